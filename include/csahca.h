@@ -481,6 +481,169 @@ typedef struct {
 
 int cp_attn_merge(const csahca_cp_merge_args* args, void* stream);
 
+/* ---- qk_norm_rope -------------------------------------------------------------
+ * [P2] Additional Techniques (query/KV RMSNorm, partial RoPE on the last dims).
+ * Norms of the query and key heads of any tokens with the position rotation in
+ * the same pass: for token (b, t) at position pos[b, t] and every head row x,
+ *   y = RoPE_pos(x / sqrt(mean(x^2) + eps) * gain)     (norm and gain only if
+ *   q_norm / k_norm; gain NULL = ones).
+ * Finished key rows are what the caches and the window ring hold.
+ * Layout: q [B, n, HQ, d], k [B, n, HK, d] with the dims of a head contiguous
+ *   and the batch, token and head strides of q_stride / k_stride (in elements,
+ *   multiples of 16 bytes, >= 0; all three 0: contiguous), so that heads may be
+ *   slices of one projection; pos [B, n] int32 on the device; gains [d] f32;
+ *   q_out [B, n, HQ, d], k_out [B, n, HK, d] contiguous (either may be its own
+ *   input where that is contiguous).  HQ or HK = 0: that side is left out.
+ *   The rows of a token with pos < 0 (padding) are left as they were.
+ * Constraints: dtype F32 (d % 4 == 0, d <= 512) or BF16 (d % 8 == 0, d <=
+ *   1024); rope_dims even, <= d and <= 512, (d - rope_dims) even.  No
+ *   workspace. */
+typedef struct {
+  int32_t dtype;
+  int32_t B, n, HQ, HK, d;
+  int32_t rope_dims;
+  float rope_base;     /* 0 -> 10000 */
+  float eps;           /* 0 -> 1e-6 */
+  int32_t q_norm, k_norm;
+  int32_t reserved0;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  const void* q;
+  const void* k;
+  const float* q_gain;
+  const float* k_gain;
+  const int32_t* pos;
+  void* q_out;
+  void* k_out;
+} csahca_norm_rope_args;
+
+int qk_norm_rope(const csahca_norm_rope_args* args, void* stream);
+
+/* ---- trees of drafted tokens ----------------------------------------------------
+ * No counterpart on the pages: speculative decoding over this library's caches.
+ * For each sequence T drafted tokens (nodes) hang on the committed tokens
+ * 0 .. pos[b] - 1 as a tree: parents[b, i] is the parent node of node i, -1 for
+ * a node that follows the last committed token, < -1 for a place that holds no
+ * node (padding).  A parent comes before its child (parents[b, i] < i); node i
+ * stands at position pos[b] + depth, and sees its own path only.  What a node
+ * gets is what a decode step gets after its path's tokens have been decoded one
+ * by one: the committed entries (pos[b] / m of them), the entries that the path
+ * itself completes, and the window over ring and path.
+ *   The rows of places without a node, of nodes below one, and of sequences
+ *   with pos[b] < 0 are left as they were.  A parent that is not below its
+ *   child raises device error 2 and the node counts as none.
+ * Constraints of both calls: 0 <= T <= CSAHCA_TREE_MAX_NODES; positions below
+ * 2^31 - 64. */
+#define CSAHCA_TREE_MAX_NODES 64
+
+/* tree_compress: the compressed entries that the nodes complete.  Node i at
+ * position t completes entry e = (t + 1) / m - 1 iff (t + 1) % m == 0; its row is
+ * pooled and finished as csa_compress / hca_compress define entry e, the
+ * tokens from pos[b] on being the path's and the earlier ones the ring's.
+ * Rows of nodes that complete nothing are left as they were.
+ * Layout: a, b, za, zb [B, T, c] the drafted tokens' raw streams (HCA: a, za);
+ *   ring [B, R, S, c] as decode_compress keeps it (R = 2m, S = 4 or R = m,
+ *   S = 2), slot p % R holding token p for the R tokens before pos[b]; bias_a,
+ *   bias_b [m, c] f32; gain [c] f32 or NULL (ones); out [B, T, c] (dtype), or
+ *   for out_dtype E4M3 codes with out_scale [B, T, c / 128] (decode_compress's
+ *   rule for indexer keys).
+ * Constraints: dtype F32 (c % 4 == 0, c <= 512) or BF16 (c % 8 == 0, c <=
+ *   1024); R <= 512; rope_dims as in csa_compress and <= 512; out_dtype =
+ *   dtype, or E4M3 with dtype BF16 and c % 128 == 0.  No workspace. */
+typedef struct {
+  int32_t kind;
+  int32_t dtype, out_dtype;
+  int32_t B, T, c;
+  int32_t m;
+  int32_t rms_norm;
+  int32_t rope_dims;
+  float rope_base;     /* 0 -> 10000 */
+  float eps;           /* 0 -> 1e-6 */
+  int32_t reserved0;
+  const int32_t* pos;
+  const int32_t* parents;
+  const void* a;
+  const void* b;
+  const void* za;
+  const void* zb;
+  const void* ring;
+  const float* bias_a;
+  const float* bias_b;
+  const float* gain;
+  void* out;
+  float* out_scale;
+} csahca_tree_compress_args;
+
+int tree_compress(const csahca_tree_compress_args* args, void* stream);
+
+/* compressed_attn_tree: attention of every node of the trees over one layer's
+ * caches.  For node i of sequence b at position t, head h:
+ *   q = RoPE_t(RMSNorm(q_raw[b, i, h]) * q_gain)            (norm only if q_norm)
+ *   compressed keys: HCA  kv_cache[b, e], e < min(N_cap, pos[b] / m), and draft[b, j]
+ *                         for every path node j that completes an entry < N_cap
+ *                    CSA  idx[b, i, :]: e < 0 skipped, e < N_cap the row
+ *                         kv_cache[b, e], N_cap + j the row draft[b, j]
+ *   window keys: positions max(0, t-w+1) .. t, from win (slot p % w, p < pos[b])
+ *     or, from pos[b] on, RoPE_p(RMSNorm(kv_raw[b, j]) * kv_gain) of the path's
+ *     nodes j                                               (norm only if kv_norm)
+ *   sink, output and its de-rotation by -t as in compressed_attn_prefill.
+ * CSA selection: idx_in [B, T, k] is used as is; without it the lightning
+ *   indexer selects the k best of the pos[b] / m committed entries (qI [B, T, HI,
+ *   dI], wI [B, T, HI] f32, kI and kI_scale as in compressed_attn_decode) and,
+ *   where draft_kI is given, of the entries that the node's path completes, by
+ *   score, ties to the lower index.  draft_kI [B, T, dI] (kI_dtype; E4M3 with
+ *   draft_kI_scale [B, T, dI / 128]) are the drafted entries' indexer keys
+ *   (tree_compress of the indexer streams).  idx_out [B, T, k] (optional)
+ *   receives the selection, ascending and -1 padded.
+ * draft [B, T, d] holds tree_compress's rows; NULL: drafted entries are no keys.
+ * Layout: q, out [B, T, H, d]; kv_cache [B, N_cap, d]; win [B, w, d]; kv_raw
+ *   [B, T, d]; pos [B], parents [B, T]; gains [d] f32 or NULL (ones); sinks [H].
+ *   out may not be q.  Cache, ring and draft rows that no node sees are not read
+ *   into any result.  With no key at all, or an infinite sink, a row is 0.
+ * Constraints: d % 32 == 0, d <= 512; rope_dims even, <= d; k <= 4096 where
+ *   draft_kI is given; caches of `dtype` rows (F32 or BF16).
+ * Workspace: csahca_tree_workspace_size(). */
+typedef struct {
+  int32_t kind;
+  int32_t dtype;
+  int32_t B, T, H, d;
+  int32_t N_cap;
+  int32_t m;
+  int32_t w;
+  int32_t k;
+  int32_t rope_dims;
+  float rope_base;     /* 0 -> 10000 */
+  float eps;           /* 0 -> 1e-6 */
+  float scale;         /* 0 -> 1/sqrt(d) */
+  int32_t q_norm, kv_norm;
+  int32_t HI, dI;
+  int32_t qI_dtype, kI_dtype;
+  const void* q;
+  const int32_t* pos;
+  const int32_t* parents;
+  const float* q_gain;
+  const float* kv_gain;
+  const void* kv_cache;
+  const void* win;
+  const void* kv_raw;
+  const void* draft;
+  const float* sinks;
+  const void* qI;
+  const float* wI;
+  const void* kI;
+  const float* kI_scale;
+  const void* draft_kI;
+  const float* draft_kI_scale;
+  const int32_t* idx_in;
+  int32_t* idx_out;
+  void* out;
+  void* workspace;
+  size_t workspace_bytes;
+} csahca_tree_attn_args;
+
+int compressed_attn_tree(const csahca_tree_attn_args* args, void* stream);
+size_t csahca_tree_workspace_size(const csahca_tree_attn_args* args);
+
 /* ---- utilities ------------------------------------------------------------ */
 
 /* Human-readable name of a status code (static string). */
@@ -491,13 +654,15 @@ int csahca_abi_version(void);
 
 /* sizeof() of the argument structs, for bindings to check their mirrors:
  * which = 0 compress, 1 indexer, 2 prefill, 3 decode, 4 decode_compress,
- * 5 cp_topk_merge, 6 cp_attn_merge; -1 for an unknown id. */
+ * 5 cp_topk_merge, 6 cp_attn_merge, 7 qk_norm_rope, 8 tree_compress,
+ * 9 compressed_attn_tree; -1 for an unknown id. */
 int64_t csahca_struct_size(int which);
 
 /* Device-side error word of the current device: every bounded wait in the
  * kernels that gives up ORs a code into it and the kernel returns early
  * instead of hanging (1: a barrier wait reached its iteration limit; 2: a
- * selection index outside [0, N) was skipped).  Synchronises `stream`, stores
+ * selection index outside [0, N) was skipped, or a tree node whose parent is
+ * not below it).  Synchronises `stream`, stores
  * the word in *code (0 = no error) and clears it.  Returns CSAHCA_OK, or
  * CSAHCA_ERR_LAUNCH if the stream itself reports a CUDA error. */
 int csahca_device_error(void* stream, int32_t* code);

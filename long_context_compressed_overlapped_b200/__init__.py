@@ -8,8 +8,11 @@ the ctypes mirror, ``synth`` the seeded synthetic inputs.
 from .api import (  # noqa: F401
     compressed_attn_decode,
     compressed_attn_prefill,
+    compressed_attn_tree,
     csa_compress,
     device_error,
     hca_compress,
     indexer_topk,
+    qk_norm_rope,
+    tree_compress,
 )

@@ -292,6 +292,205 @@ def cp_attn_merge(partials, sinks, pos, *, H, d, rope_dims, dtype=torch.bfloat16
     return out
 
 
+def _on(stream, dev):
+    """Context in which a call's tensors are allocated and its kernels launched:
+    the given stream, or the current stream of the tensors' device."""
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return torch.cuda.device(dev)
+
+
+def _arg(name, t, dev, shape, dtype, optional=False):
+    """Pointer of an argument tensor, checked for device, shape, dtype and contiguity."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ints(name, t, dev, shape, keep):
+    """Pointer of an int32 argument (other integer tensors are converted)."""
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        if t.dtype.is_floating_point or t.device != dev:
+            raise TypeError(f"{name} must be an integer tensor on {dev}")
+        t = t.to(torch.int32).contiguous()
+        keep.append(t)
+    return _arg(name, t, dev, shape, torch.int32)
+
+
+def _floats(name, t, dev, shape, keep, optional=True):
+    """Pointer of an fp32 argument (other floating tensors are converted)."""
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+        t = t.contiguous().float()
+        keep.append(t)
+    return _arg(name, t, dev, shape, torch.float32, optional)
+
+
+def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True, k_norm=True, rope_base=10000.0,
+                 eps=1e-6, q_out=None, k_out=None, stream=None):
+    """RMSNorm * gain of every query and key head and RoPE at the token's
+    position on the last rope_dims, in one pass.
+
+    q [B, n, HQ, d] and k [B, n, HK, d] (either may be None): the dims of a head
+    contiguous, the other strides free (multiples of 16 bytes), so heads may be
+    slices of one projection; pos [B, n] int32, negative for padding (the rows
+    of such a token are left as they were).  q_out / k_out: contiguous, by
+    default new; a contiguous input may be its own output.  Returns (q_out, k_out)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k is required")
+    dev, dt, keep = x.device, x.dtype, []
+    code = _dt(x)
+    B, n, _, d = x.shape
+    with _on(stream, dev):
+        a = N.NormRopeArgs(dtype=code, B=B, n=n, d=d, rope_dims=rope_dims, rope_base=rope_base, eps=eps,
+                           q_norm=int(bool(q_norm)), k_norm=int(bool(k_norm)), pos=_ints("pos", pos, dev, (B, n), keep))
+        outs = []
+        for name, t, o, gain in (("q", q, q_out, q_gain), ("k", k, k_out, k_gain)):
+            if t is None:
+                outs.append(None)
+                continue
+            if t.device != dev or t.dtype != dt or t.dim() != 4 or (t.shape[0], t.shape[1], t.shape[3]) != (B, n, d):
+                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} does not match the other rows")
+            if d > 1 and t.stride(3) != 1:
+                raise ValueError(f"{name}: the dims of a head must be contiguous")
+            if o is None:
+                o = torch.empty(t.shape, dtype=dt, device=dev)
+            setattr(a, "H" + name.upper(), t.shape[2])
+            if not t.is_contiguous():
+                setattr(a, name + "_stride", (N.i64 * 3)(*t.stride()[:3]))
+            setattr(a, name, t.data_ptr())
+            setattr(a, name + "_out", _arg(name + "_out", o, dev, t.shape, dt))
+            setattr(a, name + "_gain", _floats(name + "_gain", gain, dev, (d,), keep))
+            outs.append(o)
+        N.check(N.lib().qk_norm_rope(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "qk_norm_rope")
+    return tuple(outs)
+
+
+def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, gain=None, rms_norm=True, rope_dims=0,
+                  rope_base=10000.0, eps=1e-6, out=None, out_scale=None, stream=None):
+    """The compressed entries that the nodes of draft trees complete.
+
+    streams: (a, b, za, zb) for "csa" or (a, za) for "hca", each [B, T, c], the
+    drafted tokens' raw streams; ring [B, R, S, c] as decode_compress keeps it;
+    pos [B] the first drafted token's position; parents [B, T] (parent node, -1
+    for a node that follows the last committed token, < -1 for no node).
+    out [B, T, c]: row i is written iff node i's token ends a block, the others
+    are left as they were (a new out starts at zero).  With out_scale
+    [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys."""
+    csa = kind == "csa"
+    if len(streams) != (4 if csa else 2):
+        raise ValueError("csa takes four streams (a, b, za, zb), hca two (a, za)")
+    x = streams[0]
+    dev, dt, keep = x.device, x.dtype, []
+    code = _dt(x)
+    B, T, c = x.shape
+    R, S = (2 * m, 4) if csa else (m, 2)
+    with _on(stream, dev):
+        f8 = out_scale is not None
+        odt = torch.uint8 if f8 else dt
+        if out is None:
+            out = torch.zeros(B, T, c, dtype=odt, device=dev)
+        p = [_arg(f"streams[{i}]", t, dev, (B, T, c), dt) for i, t in enumerate(streams)]
+        a = N.TreeCompressArgs(
+            kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
+            rms_norm=int(bool(rms_norm)), rope_dims=rope_dims, rope_base=rope_base, eps=eps,
+            pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
+            a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
+            ring=_arg("ring", ring, dev, (B, R, S, c), dt), bias_a=_floats("bias_a", bias_a, dev, (m, c), keep, False),
+            bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
+            out=_arg("out", out, dev, (B, T, c), odt),
+            out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
+        N.check(N.lib().tree_compress(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "tree_compress")
+    return out
+
+
+def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, rope_dims, draft=None, k=0, qI=None,
+                   wI=None, kI=None, kI_scale=None, draft_kI=None, draft_kI_scale=None, idx_in=None, idx_out=None,
+                   q_gain=None, kv_gain=None, q_norm=True, kv_norm=True, rope_base=10000.0, eps=1e-6, scale=0.0,
+                   out=None):
+    """Build the TreeAttnArgs struct (and keep the tensors it points to alive
+    in the returned list).  Returns (args, out, keep)."""
+    csa = kind == "csa"
+    dev, dt, keep = q.device, q.dtype, []
+    code = _dt(q)
+    B, T, H, d = q.shape
+    Nc = kv_cache.shape[1]
+    w = win.shape[1] if win is not None else 0
+    if out is None:
+        out = torch.zeros(q.shape, dtype=dt, device=dev)
+    a = N.TreeAttnArgs(kind=N.CSA if csa else N.HCA, dtype=code, B=B, T=T, H=H, d=d, N_cap=Nc, m=m, w=w,
+                       rope_dims=rope_dims, rope_base=rope_base, eps=eps, scale=scale, q_norm=int(bool(q_norm)),
+                       kv_norm=int(bool(kv_norm)), q=_arg("q", q, dev, q.shape, dt),
+                       pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
+                       q_gain=_floats("q_gain", q_gain, dev, (d,), keep),
+                       kv_gain=_floats("kv_gain", kv_gain, dev, (d,), keep),
+                       kv_cache=_arg("kv_cache", kv_cache, dev, (B, Nc, d), dt) if Nc else None,
+                       draft=_arg("draft", draft, dev, (B, T, d), dt, True),
+                       sinks=_floats("sinks", sinks, dev, (H,), keep, False), out=_arg("out", out, dev, q.shape, dt))
+    if w:
+        a.win = _arg("win", win, dev, (B, w, d), dt)
+        a.kv_raw = _arg("kv_raw", kv_raw, dev, (B, T, d), dt)
+    if csa:
+        if idx_in is not None:
+            k = idx_in.shape[2]
+            a.idx_in = _arg("idx_in", idx_in, dev, (B, T, k), torch.int32)
+        else:
+            if qI is None or wI is None or kI is None:
+                raise ValueError("csa needs idx_in, or qI, wI and kI for the indexer")
+            HI, dI = qI.shape[2:]
+            a.HI, a.dI, a.qI_dtype, a.kI_dtype = HI, dI, _dt(qI), _dt(kI)
+            a.qI = _arg("qI", qI, dev, (B, T, HI, dI), qI.dtype)
+            a.wI = _floats("wI", wI, dev, (B, T, HI), keep, False)
+            a.kI = _arg("kI", kI, dev, (B, Nc, dI), kI.dtype) if Nc else None
+            a.kI_scale = _floats("kI_scale", kI_scale, dev, (B, Nc, dI // 128), keep)
+            a.draft_kI = _arg("draft_kI", draft_kI, dev, (B, T, dI), kI.dtype, True)
+            a.draft_kI_scale = _floats("draft_kI_scale", draft_kI_scale, dev, (B, T, dI // 128), keep)
+        a.k = k
+        a.idx_out = _arg("idx_out", idx_out, dev, (B, T, k), torch.int32, True)
+    return a, out, keep
+
+
+def compressed_attn_tree(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, rope_dims, workspace=None,
+                         stream=None, **kw):
+    """Attention of every node of draft trees over one CSA or HCA layer's caches:
+    what decode steps along each node's own path would return, in one call.
+
+    q [B, T, H, d] raw queries of the drafted tokens; pos [B] the first drafted
+    token's position; parents [B, T] as in tree_compress; kv_cache [B, N_cap, d],
+    win [B, w, d] (the committed tokens'); kv_raw [B, T, d] the drafted tokens'
+    raw window rows; draft [B, T, d] the entries they complete (tree_compress).
+    CSA: idx_in [B, T, k] (N_cap + j names draft row j), or k with qI, wI, kI
+    (kI_scale) and draft_kI (draft_kI_scale) for the lightning indexer; idx_out
+    [B, T, k] receives the selection.  Rows of places without a node are left as
+    they were (a new out starts at zero).  Returns out [B, T, H, d]."""
+    dev = q.device
+    with _on(stream, dev):
+        a, out, keep = tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, m=m, rope_dims=rope_dims, **kw)
+        L = N.lib()
+        nbytes = L.csahca_tree_workspace_size(C.byref(a))
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        a.workspace = _arg("workspace", workspace, dev, workspace.shape, workspace.dtype)
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+        N.check(L.compressed_attn_tree(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "compressed_attn_tree")
+    del keep
+    return out
+
+
 def device_error(stream=None) -> int:
     """Synchronise the stream and return (and clear) the device error word."""
     code = N.i32(0)

@@ -25,6 +25,10 @@
 #include "attention_tc.cuh"
 #include "context_parallel.cuh"
 #include "attention_small_tc.cuh"
+#include "norm_rope.cuh"
+#include "tree_compress.cuh"
+#include "tree_select.cuh"
+#include "attention_tree_tc.cuh"
 
 using namespace csahca;
 
@@ -714,13 +718,13 @@ int launch_finish(const void* x, void* out, const float* gain, int64_t rows, int
   return CSAHCA_OK;
 }
 
-template <typename T>
+template <typename T, bool kTree = false>
 int launch_simt_attn(const SimtAttnParams& p, int nq_total, cudaStream_t s, const char* name) {
   const size_t smem = ((size_t)kSimtHG * p.d + (size_t)kSimtKeys * (p.d + 1)) * sizeof(float);
-  cudaFuncSetAttribute(attn_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaFuncSetAttribute(attn_simt_kernel<T, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   dim3 grid((unsigned)nq_total, (unsigned)ceil_div64(p.H, kSimtHG), (unsigned)p.splits);
   CSAHCA_TRACE(name, s);
-  launch_k(attn_simt_kernel<T>, dim3(grid), dim3(32 * kSimtHG), smem, s, p);
+  launch_k(attn_simt_kernel<T, kTree>, dim3(grid), dim3(32 * kSimtHG), smem, s, p);
   CSAHCA_CHECK_LAUNCH();
   return CSAHCA_OK;
 }
@@ -1101,7 +1105,7 @@ int run_decode_t(const csahca_decode_args* a, cudaStream_t s, char* ws) {
   CombineParams c;
   c.partial = partial; c.sinks = a->sinks; c.pos = a->pos; c.out = a->out;
   c.B = a->B; c.nq = 1; c.H = a->H; c.d = a->d; c.splits = L.splits;
-  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base;
+  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base; c.tree = 0;
   {
     CSAHCA_TRACE("attn_combine", s);
     launch_k(attn_combine_kernel<T>, dim3((unsigned)(a->B * a->H)), dim3(128), 0, s, c);
@@ -1262,6 +1266,439 @@ int run_cp_attn_merge(const csahca_cp_merge_args* a, void* stream) {
   return CSAHCA_OK;
 }
 
+// ------------------------------------------------------------ qk_norm_rope --
+
+// theta of the first r / 2 pairs, in double, into a kernel parameter array.
+void rope_theta_pairs(double* theta, int r, double base) {
+  for (int j = 0; j < r / 2; ++j) theta[j] = pow(base, -2.0 * j / r);
+}
+
+template <typename T, int LPR, int NCH, bool kTree>
+void launch_norm_rope_t(NormRopeParams& p, int64_t tokens, cudaStream_t s) {
+  // about four CTAs an SM or a whole token a CTA, whichever is fewer CTAs
+  constexpr int RPC = kNrThreads / LPR;
+  const int rows = p.heads[0] + p.heads[1];
+  int64_t groups = ceil_div64(4 * num_sms(), tokens);
+  const int64_t most = ceil_div64(rows, RPC);
+  if (groups > most) groups = most;
+  if (groups < 1) groups = 1;
+  p.rows_per_cta = (int)(ceil_div64(ceil_div64(rows, groups), RPC) * RPC);
+  groups = rows > 0 ? ceil_div64(rows, p.rows_per_cta) : 1;
+  CSAHCA_TRACE(kTree ? "tree_norm_rope" : "qk_norm_rope", s);
+  launch_k(norm_rope_kernel<T, LPR, NCH, kTree>, dim3((unsigned)tokens, (unsigned)groups), dim3(kNrThreads), 0, s, p);
+}
+
+template <typename T, bool kTree>
+int launch_norm_rope(NormRopeParams& p, int64_t tokens, cudaStream_t s) {
+  const int nch = p.d / Vec16<T>::N;
+  if (nch <= 8) launch_norm_rope_t<T, 8, 1, kTree>(p, tokens, s);
+  else if (nch <= 16) launch_norm_rope_t<T, 16, 1, kTree>(p, tokens, s);
+  else if (nch <= 32) launch_norm_rope_t<T, 32, 1, kTree>(p, tokens, s);
+  else if (nch <= 64) launch_norm_rope_t<T, 32, 2, kTree>(p, tokens, s);
+  else launch_norm_rope_t<T, 32, 4, kTree>(p, tokens, s);
+  CSAHCA_CHECK_LAUNCH();
+  return CSAHCA_OK;
+}
+
+int run_norm_rope(const csahca_norm_rope_args* a, void* stream) {
+  if (!a) return CSAHCA_ERR_INVALID_ARG;
+  if (a->dtype != CSAHCA_F32 && a->dtype != CSAHCA_BF16) return CSAHCA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->n < 0 || a->HQ < 0 || a->HK < 0 || a->d < 1) return CSAHCA_ERR_INVALID_ARG;
+  if (a->rope_dims < 0 || a->rope_dims > a->d || (a->rope_dims & 1) || ((a->d - a->rope_dims) & 1))
+    return CSAHCA_ERR_INVALID_ARG;
+  const int vec = 16 / dtype_size(a->dtype);
+  if (a->d % vec || a->d > 128 * vec || a->rope_dims > 2 * kNrMaxPairs) return CSAHCA_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * a->n > INT32_MAX || (int64_t)a->HQ + a->HK > 65535) return CSAHCA_ERR_UNSUPPORTED;
+  NormRopeParams p;
+  memset(&p, 0, sizeof(p));
+  p.heads[0] = a->HQ; p.heads[1] = a->HK;
+  p.x[0] = a->q; p.x[1] = a->k;
+  p.y[0] = a->q_out; p.y[1] = a->k_out;
+  p.gain[0] = a->q_gain; p.gain[1] = a->k_gain;
+  p.norm[0] = a->q_norm; p.norm[1] = a->k_norm;
+  const int64_t* st[2] = {a->q_stride, a->k_stride};
+  bool any = false;
+  for (int k = 0; k < 2; ++k) {
+    const int64_t own[3] = {(int64_t)a->n * p.heads[k] * a->d, (int64_t)p.heads[k] * a->d, a->d};
+    const bool dense = !st[k][0] && !st[k][1] && !st[k][2];
+    bool same = true;
+    for (int x = 0; x < 3; ++x) {
+      if (st[k][x] < 0) return CSAHCA_ERR_INVALID_ARG;
+      if (st[k][x] % vec) return CSAHCA_ERR_ALIGNMENT;
+      p.xs[k][x] = dense ? own[x] : st[k][x];
+      p.ys[k][x] = own[x];
+      same = same && p.xs[k][x] == own[x];
+    }
+    if (p.heads[k] && a->B && a->n) {
+      if (!p.x[k] || !p.y[k]) return CSAHCA_ERR_INVALID_ARG;
+      if (p.x[k] == p.y[k] && !same) return CSAHCA_ERR_INVALID_ARG;   // in place: contiguous rows only
+      any = true;
+    }
+  }
+  if (!any) return CSAHCA_OK;
+  if (!a->pos) return CSAHCA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a->q, a->k, a->q_gain, a->k_gain, a->pos, a->q_out, a->k_out};
+  for (const void* x : ptrs)
+    if (x && !aligned16(x)) return CSAHCA_ERR_ALIGNMENT;
+  const int ok = device_ok();
+  if (ok != CSAHCA_OK) return ok;
+  p.pos = a->pos; p.n = a->n; p.d = a->d; p.rope_dims = a->rope_dims;
+  p.eps = a->eps > 0 ? a->eps : kDefaultEps;
+  rope_theta_pairs(p.theta, a->rope_dims, a->rope_base > 0 ? a->rope_base : kDefaultRopeBase);
+  const int64_t tokens = (int64_t)a->B * a->n;
+  cudaStream_t s = as_stream(stream);
+  return a->dtype == CSAHCA_F32 ? launch_norm_rope<float, false>(p, tokens, s)
+                                : launch_norm_rope<__nv_bfloat16, false>(p, tokens, s);
+}
+
+// ------------------------------------------------------------ tree_compress --
+
+template <typename T, bool kCSA>
+void launch_tree_compress(const TreeCompressParams& p, int nodes, cudaStream_t s) {
+  constexpr int smem = tree_compress_smem<T>();
+  cudaFuncSetAttribute(tree_compress_kernel<T, kCSA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  CSAHCA_TRACE("tree_compress", s);
+  launch_k(tree_compress_kernel<T, kCSA>, dim3((unsigned)nodes), dim3(kTcpThreads), smem, s, p);
+}
+
+int run_tree_compress(const csahca_tree_compress_args* a, void* stream) {
+  if (!a) return CSAHCA_ERR_INVALID_ARG;
+  if (a->kind != CSAHCA_CSA && a->kind != CSAHCA_HCA) return CSAHCA_ERR_INVALID_ARG;
+  if (a->dtype != CSAHCA_F32 && a->dtype != CSAHCA_BF16) return CSAHCA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->T < 0 || a->c < 1 || a->m < 1) return CSAHCA_ERR_INVALID_ARG;
+  if (a->rope_dims < 0 || a->rope_dims > a->c || (a->rope_dims & 1) || ((a->c - a->rope_dims) & 1))
+    return CSAHCA_ERR_INVALID_ARG;
+  const bool csa = a->kind == CSAHCA_CSA, f8 = a->out_dtype == CSAHCA_E4M3;
+  const int vec = 16 / dtype_size(a->dtype);
+  if (!f8 && a->out_dtype != a->dtype) return CSAHCA_ERR_UNSUPPORTED;
+  if (f8 && (a->dtype != CSAHCA_BF16 || a->c % 128)) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->c % vec || a->c > 128 * vec || a->rope_dims > 2 * kNrMaxPairs) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->T > CSAHCA_TREE_MAX_NODES || a->m > kTcpMaxTokens / (csa ? 2 : 1)) return CSAHCA_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * a->T > INT32_MAX) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->B == 0 || a->T == 0) return CSAHCA_OK;
+  if (!a->pos || !a->parents || !a->a || !a->za || !a->ring || !a->bias_a || !a->out) return CSAHCA_ERR_INVALID_ARG;
+  if (csa && (!a->b || !a->zb || !a->bias_b)) return CSAHCA_ERR_INVALID_ARG;
+  if (f8 && !a->out_scale) return CSAHCA_ERR_INVALID_ARG;
+  const void* ptrs[] = {a->pos, a->parents, a->a, a->b, a->za, a->zb, a->ring, a->bias_a, a->bias_b, a->gain,
+                        a->out, a->out_scale};
+  for (const void* x : ptrs)
+    if (x && !aligned16(x)) return CSAHCA_ERR_ALIGNMENT;
+  const int ok = device_ok();
+  if (ok != CSAHCA_OK) return ok;
+  TreeCompressParams p;
+  memset(&p, 0, sizeof(p));
+  p.parents = a->parents; p.pos = a->pos;
+  p.nw[0] = a->a; p.nw[1] = csa ? a->b : a->za; p.nw[2] = csa ? a->za : nullptr; p.nw[3] = csa ? a->zb : nullptr;
+  p.ring = a->ring; p.bias_a = a->bias_a; p.bias_b = a->bias_b; p.gain = a->gain;
+  p.out = a->out; p.out_scale = a->out_scale;
+  p.T = a->T; p.c = a->c; p.m = a->m; p.rms_norm = a->rms_norm; p.rope_dims = a->rope_dims; p.e4m3 = f8 ? 1 : 0;
+  p.eps = a->eps > 0 ? a->eps : kDefaultEps;
+  rope_theta_pairs(p.theta, a->rope_dims, a->rope_base > 0 ? a->rope_base : kDefaultRopeBase);
+  cudaStream_t s = as_stream(stream);
+  const int nodes = a->B * a->T;
+  if (a->dtype == CSAHCA_F32) {
+    if (csa) launch_tree_compress<float, true>(p, nodes, s);
+    else launch_tree_compress<float, false>(p, nodes, s);
+  } else {
+    if (csa) launch_tree_compress<__nv_bfloat16, true>(p, nodes, s);
+    else launch_tree_compress<__nv_bfloat16, false>(p, nodes, s);
+  }
+  CSAHCA_CHECK_LAUNCH();
+  return CSAHCA_OK;
+}
+
+// ----------------------------------------------------- compressed_attn_tree --
+
+bool tree_tc(const csahca_tree_attn_args* a) {
+  return a->dtype == CSAHCA_BF16 && a->H == kAttnH && a->d == kAttnD && a->rope_dims <= 128;
+}
+
+csahca_indexer_args tree_indexer_args(const csahca_tree_attn_args* a) {
+  csahca_indexer_args ia;
+  memset(&ia, 0, sizeof(ia));
+  ia.q_dtype = a->qI_dtype; ia.k_dtype = a->kI_dtype; ia.B = a->B; ia.nq = a->T; ia.HI = a->HI; ia.dI = a->dI;
+  ia.N = a->N_cap; ia.m = a->m; ia.k = a->k;
+  ia.qI = a->qI; ia.w = a->wI; ia.kI = a->kI; ia.kI_scale = a->kI_scale;
+  return ia;
+}
+
+int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
+  if (!a) return CSAHCA_ERR_INVALID_ARG;
+  if (a->kind != CSAHCA_CSA && a->kind != CSAHCA_HCA) return CSAHCA_ERR_INVALID_ARG;
+  if (a->dtype != CSAHCA_F32 && a->dtype != CSAHCA_BF16) return CSAHCA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->T < 0 || a->H < 1 || a->d < 1 || a->N_cap < 0 || a->m < 1 || a->w < 0)
+    return CSAHCA_ERR_INVALID_ARG;
+  if (a->rope_dims < 0 || a->rope_dims > a->d || (a->rope_dims & 1)) return CSAHCA_ERR_INVALID_ARG;
+  if (a->T > CSAHCA_TREE_MAX_NODES || a->d % 32 || a->d > 32 * kSimtMaxDPL) return CSAHCA_ERR_UNSUPPORTED;
+  // row codes and tensor coordinates are 32-bit
+  if ((int64_t)a->B * a->T * a->H > INT32_MAX || (int64_t)a->B * a->N_cap > INT32_MAX ||
+      (int64_t)a->B * a->w > kRowMask || (int64_t)a->B * a->T > kRowMask)
+    return CSAHCA_ERR_UNSUPPORTED;
+  const bool csa = a->kind == CSAHCA_CSA;
+  if (csa) {
+    if (a->k < 1) return CSAHCA_ERR_INVALID_ARG;
+    if ((int64_t)a->k + a->w + a->T > INT32_MAX / 2) return CSAHCA_ERR_UNSUPPORTED;
+    if (!a->idx_in) {
+      const csahca_indexer_args ia = tree_indexer_args(a);
+      const int st = validate_indexer(&ia, /*shapes_only=*/true);
+      if (st != CSAHCA_OK) return st;
+      if (a->draft_kI && a->k > kTsMaxK) return CSAHCA_ERR_UNSUPPORTED;
+    }
+  }
+  if (shapes_only || a->B == 0 || a->T == 0) return CSAHCA_OK;
+  if (!a->q || !a->pos || !a->parents || !a->sinks || !a->out || a->out == a->q) return CSAHCA_ERR_INVALID_ARG;
+  if (a->N_cap > 0 && !a->kv_cache) return CSAHCA_ERR_INVALID_ARG;
+  if (a->w > 0 && (!a->win || !a->kv_raw)) return CSAHCA_ERR_INVALID_ARG;
+  if (csa && !a->idx_in) {
+    if (!a->qI || !a->wI || (a->N_cap > 0 && !a->kI)) return CSAHCA_ERR_INVALID_ARG;
+    if (a->kI_dtype == CSAHCA_E4M3 && ((a->N_cap > 0 && !a->kI_scale) || (a->draft_kI && !a->draft_kI_scale)))
+      return CSAHCA_ERR_INVALID_ARG;
+    if (a->draft_kI && !a->draft) return CSAHCA_ERR_INVALID_ARG;   // a selected drafted entry needs its row
+  }
+  const void* ptrs[] = {a->q, a->pos, a->parents, a->q_gain, a->kv_gain, a->kv_cache, a->win, a->kv_raw, a->draft,
+                        a->sinks, a->qI, a->wI, a->kI, a->kI_scale, a->draft_kI, a->draft_kI_scale, a->idx_in,
+                        a->idx_out, a->out, a->workspace};
+  for (const void* x : ptrs)
+    if (x && !aligned16(x)) return CSAHCA_ERR_ALIGNMENT;
+  return CSAHCA_OK;
+}
+
+struct TreeLayout {
+  size_t node_pos, sel_pos, info, list, rows, q, sel_scores, idx, indexer, indexer_bytes, partial, total;
+  bool tc;
+  int splits, keys_per_split;
+};
+
+// Splits of a node's tiles: `nodes` x s items over the SMs in waves, an item
+// costing its tiles and about two tiles' time of its own (query load, first
+// tile's latency, epilogue), a join about three more.
+int tree_splits(int64_t nodes, int tiles) {
+  const int sms = num_sms();
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= tiles && s <= kTreeMaxSplits && (s == 1 || nodes * s <= 8 * (int64_t)sms); ++s) {
+    const double waves = (double)ceil_div64(nodes * s, sms);
+    const double cost = waves * ((double)ceil_div64(tiles, s) + 2.0) + (s > 1 ? 3.0 + 0.01 * (double)(nodes * s) : 0.0);
+    if (cost < best_cost) { best_cost = cost; best = s; }
+  }
+  return best;
+}
+
+TreeLayout tree_layout(const csahca_tree_attn_args* a) {
+  TreeLayout L;
+  const bool csa = a->kind == CSAHCA_CSA;
+  const int64_t nodes = (int64_t)a->B * a->T;
+  const size_t e = dtype_size(a->dtype);
+  L.tc = tree_tc(a);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += align_up(bytes, 256); return at; };
+  L.node_pos = take(nodes * 4);
+  L.sel_pos = take(nodes * 4);
+  L.info = take(nodes * 16);
+  L.list = take((size_t)nodes * (a->w + a->T) * 4);
+  L.rows = take(nodes * a->d * e);
+  L.q = L.tc ? take((size_t)nodes * a->H * a->d * e) : off;
+  const bool select = csa && !a->idx_in;
+  L.sel_scores = select && a->draft_kI ? take((size_t)nodes * a->k * 4) : off;
+  L.idx = select && !a->idx_out ? take((size_t)nodes * a->k * 4) : off;
+  L.indexer = off;
+  L.indexer_bytes = 0;
+  if (select) {
+    const csahca_indexer_args ia = tree_indexer_args(a);
+    L.indexer_bytes = indexer_workspace(&ia);
+    take(L.indexer_bytes);
+  }
+  const int64_t jmax = (csa ? (int64_t)a->k : (int64_t)a->N_cap) + a->w + (csa ? 0 : a->T);
+  L.keys_per_split = 0;
+  if (L.tc) {
+    const int64_t tiles = csa ? ceil_div64((int64_t)a->k + a->w, 128)
+                              : a->N_cap / 128 + ceil_div64((int64_t)(a->N_cap & 127) + a->w, 128);
+    L.splits = tree_splits(nodes, (int)(tiles > 0 ? tiles : 1));
+    L.partial = L.splits > 1 ? take((size_t)nodes * L.splits * kTcPartialBytes) : off;
+  } else {
+    const int64_t ctas = nodes * ceil_div64(a->H, kSimtHG);
+    int64_t s = ceil_div64(4 * num_sms(), ctas > 0 ? ctas : 1);
+    const int64_t most = jmax > 0 ? ceil_div64(jmax, 128) : 1;
+    if (s > most) s = most;
+    if (s > kCombineMaxSplits) s = kCombineMaxSplits;
+    L.splits = (int)(s < 1 ? 1 : s);
+    L.keys_per_split = (int)(jmax > 0 ? ceil_div64(jmax, L.splits) : 1);
+    L.partial = L.splits > 1 ? take((size_t)nodes * a->H * L.splits * (a->d + 4) * 4) : off;
+  }
+  L.total = off;
+  return L;
+}
+
+int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws, const int32_t* sel, float scale,
+                   double base, cudaStream_t s) {
+  const int nodes = a->B * a->T;
+  TreeAttnParams p;
+  memset(&p, 0, sizeof(p));
+  __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(ws + L.q);
+  p.kv = a->N_cap > 0 ? static_cast<const __nv_bfloat16*>(a->kv_cache) : q;
+  p.rows[ROW_RING] = static_cast<const __nv_bfloat16*>(a->win);
+  p.rows[ROW_TREE] = reinterpret_cast<const __nv_bfloat16*>(ws + L.rows);
+  p.rows[ROW_DRAFT] = static_cast<const __nv_bfloat16*>(a->draft);
+  p.idx = sel; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
+  p.sinks = a->sinks; p.list_stride = a->w + a->T; p.k = a->k; p.N = a->N_cap; p.T = a->T;
+  p.splits = L.splits; p.n_items = nodes * L.splits; p.scale_log2 = scale * kLog2e; p.rope_dims = a->rope_dims;
+  p.out = static_cast<__nv_bfloat16*>(a->out); p.partial = ws + L.partial;
+  rope_theta_table(p.theta, a->rope_dims, base);
+  // rows of 512 bf16 as [chunk 8][row][64]: a key box is two chunks of 128
+  // rows (32 KB), the query box all 8 chunks of a node's 64 heads
+  CUtensorMap m_rows, m_q, m_part;
+  const uint64_t rs = kAttnD * 2;
+  if (!encode_3d(&m_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, 64, (uint64_t)nodes * kAttnH, kAttnChunks, rs, 128, 64,
+                 kAttnH, kAttnChunks, CU_TENSOR_MAP_SWIZZLE_128B))
+    return CSAHCA_ERR_LAUNCH;
+  m_rows = m_q;
+  m_part = m_q;
+  const uint64_t comp_rows = (uint64_t)a->B * a->N_cap;
+  if (!sel && comp_rows >= 128 &&
+      !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->kv_cache, 64, comp_rows, kAttnChunks, rs, 128, 64, 128,
+                 2, CU_TENSOR_MAP_SWIZZLE_128B))
+    return CSAHCA_ERR_LAUNCH;
+  if (L.splits > 1 &&
+      !encode_2d(&m_part, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.partial, kAttnH, (uint64_t)p.n_items * kTcPartialRows,
+                 kAttnH, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    return CSAHCA_ERR_LAUNCH;
+  cudaFuncSetAttribute(attn_tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem::TOTAL);
+  // the register split must fit the launch allocation (an increase would wait)
+  static int launch_regs = -1;
+  if (launch_regs < 0) {
+    cudaFuncAttributes fa;
+    launch_regs = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel) == cudaSuccess ? fa.numRegs : 0;
+  }
+  if ((int64_t)launch_regs * kTreeThreads <
+      256 * kAttnRegsSoftmax + 32 * kTreeProducers * kAttnRegsProducer + 128 * kAttnRegsMma)
+    return CSAHCA_ERR_UNSUPPORTED;
+  const int grid = p.n_items < num_sms() ? p.n_items : num_sms();
+  {
+    CSAHCA_TRACE(sel ? "attn_tree_csa_tc" : "attn_tree_hca_tc", s);
+    launch_k(attn_tree_tc_kernel, dim3((unsigned)grid), dim3(kTreeThreads), AttnSmem::TOTAL, s, m_rows, m_q, m_part, p);
+  }
+  CSAHCA_CHECK_LAUNCH();
+  if (L.splits > 1) {
+    TreeCombineParams c;
+    memset(&c, 0, sizeof(c));
+    c.partial = p.partial; c.sinks = a->sinks; c.node_pos = reinterpret_cast<const int*>(ws + L.node_pos);
+    c.out = p.out; c.splits = L.splits; c.rope_dims = a->rope_dims;
+    memcpy(c.theta, p.theta, sizeof(c.theta));
+    CSAHCA_TRACE("attn_tree_combine", s);
+    launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / 64), dim3(kTreeCombineThreads), 0, s, c);
+    CSAHCA_CHECK_LAUNCH();
+  }
+  return CSAHCA_OK;
+}
+
+template <typename T>
+int run_tree_t(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws, cudaStream_t s) {
+  const bool csa = a->kind == CSAHCA_CSA;
+  const int nodes = a->B * a->T;
+  const double base = a->rope_base > 0 ? a->rope_base : kDefaultRopeBase;
+  const float eps = a->eps > 0 ? a->eps : kDefaultEps;
+  const float scale = a->scale > 0 ? a->scale : 1.0f / sqrtf((float)a->d);
+  int* node_pos = reinterpret_cast<int*>(ws + L.node_pos);
+  int* sel_pos = reinterpret_cast<int*>(ws + L.sel_pos);
+  int4* info = reinterpret_cast<int4*>(ws + L.info);
+  int* list = reinterpret_cast<int*>(ws + L.list);
+  int st;
+  {
+    // the nodes' plan, their finished window rows, and (tensor-core path) queries
+    NormRopeParams p;
+    memset(&p, 0, sizeof(p));
+    p.heads[0] = L.tc ? a->H : 0;
+    p.heads[1] = a->w > 0 ? 1 : 0;
+    const void* x[2] = {a->q, a->kv_raw};
+    void* y[2] = {ws + L.q, ws + L.rows};
+    for (int k = 0; k < 2; ++k) {
+      p.x[k] = x[k]; p.y[k] = y[k];
+      p.xs[k][0] = p.ys[k][0] = (int64_t)a->T * p.heads[k] * a->d;
+      p.xs[k][1] = p.ys[k][1] = (int64_t)p.heads[k] * a->d;
+      p.xs[k][2] = p.ys[k][2] = a->d;
+    }
+    p.gain[0] = a->q_gain; p.gain[1] = a->kv_gain;
+    p.norm[0] = a->q_norm; p.norm[1] = a->kv_norm;
+    p.n = a->T; p.d = a->d; p.rope_dims = a->rope_dims; p.eps = eps;
+    TreePlan& t = p.plan;
+    t.parents = a->parents; t.pos = a->pos; t.T = a->T; t.w = a->w; t.m = a->m; t.N = a->N_cap;
+    t.list_drafts = !csa && a->draft ? 1 : 0;
+    t.node_pos = node_pos; t.sel_pos = sel_pos; t.list = list; t.info = info;
+    rope_theta_pairs(p.theta, a->rope_dims, base);
+    st = launch_norm_rope<T, true>(p, nodes, s);
+    if (st != CSAHCA_OK) return st;
+  }
+  const int32_t* sel = nullptr;
+  if (csa && a->idx_in) {
+    sel = a->idx_in;
+    if (a->idx_out && a->idx_out != a->idx_in &&
+        cudaMemcpyAsync(a->idx_out, a->idx_in, (size_t)nodes * a->k * 4, cudaMemcpyDeviceToDevice, s) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return CSAHCA_ERR_LAUNCH;
+    }
+  } else if (csa) {
+    int32_t* idx = a->idx_out ? a->idx_out : reinterpret_cast<int32_t*>(ws + L.idx);
+    csahca_indexer_args ia = tree_indexer_args(a);
+    ia.q_pos = sel_pos; ia.idx = idx;
+    ia.sel_scores = a->draft_kI ? reinterpret_cast<float*>(ws + L.sel_scores) : nullptr;
+    ia.workspace = ws + L.indexer; ia.workspace_bytes = L.indexer_bytes;
+    st = run_indexer(&ia, s);
+    if (st != CSAHCA_OK) return st;
+    if (a->draft_kI) {
+      TreeSelectParams p;
+      memset(&p, 0, sizeof(p));
+      p.parents = a->parents; p.pos = a->pos; p.qI = a->qI; p.w = a->wI; p.kI = a->draft_kI;
+      p.kI_scale = a->draft_kI_scale; p.q_bf16 = a->qI_dtype == CSAHCA_BF16;
+      p.k_dtype = a->kI_dtype == CSAHCA_F32 ? 0 : a->kI_dtype == CSAHCA_BF16 ? 1 : 2;
+      p.T = a->T; p.HI = a->HI; p.dI = a->dI; p.m = a->m; p.N = a->N_cap; p.k = a->k;
+      p.scores = ia.sel_scores; p.idx = idx;
+      CSAHCA_TRACE("tree_select", s);
+      launch_k(tree_select_kernel, dim3((unsigned)nodes), dim3(kTsThreads), (size_t)a->k * 8, s, p);
+      CSAHCA_CHECK_LAUNCH();
+    }
+    sel = idx;
+  }
+  if constexpr (sizeof(T) == 2) {
+    if (L.tc) return launch_tree_tc(a, L, ws, sel, scale, base, s);
+  }
+  SimtAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = a->q; p.q_gain = a->q_gain; p.sinks = a->sinks; p.pos = node_pos;
+  p.q_norm = a->q_norm; p.eps = eps; p.scale = scale; p.rope_dims = a->rope_dims; p.rope_base = base;
+  p.B = a->B; p.nq = a->T; p.H = a->H; p.d = a->d;
+  p.kv_comp = a->kv_cache; p.N = a->N_cap; p.idx = sel; p.k = a->k; p.m = a->m; p.w = a->w;
+  p.splits = L.splits; p.keys_per_split = L.keys_per_split;
+  p.out = a->out; p.partial = L.splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
+  p.tree_rows[ROW_RING] = a->win; p.tree_rows[ROW_TREE] = ws + L.rows; p.tree_rows[ROW_DRAFT] = a->draft;
+  p.list = list; p.info = info; p.list_stride = a->w + a->T;
+  st = launch_simt_attn<T, true>(p, nodes, s, csa ? "attn_tree_csa_simt" : "attn_tree_hca_simt");
+  if (st != CSAHCA_OK || L.splits == 1) return st;
+  CombineParams c;
+  memset(&c, 0, sizeof(c));
+  c.partial = p.partial; c.sinks = a->sinks; c.pos = node_pos; c.out = a->out;
+  c.B = nodes; c.nq = 1; c.H = a->H; c.d = a->d; c.splits = L.splits;
+  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base; c.tree = 1;
+  {
+    CSAHCA_TRACE("attn_tree_combine", s);
+    launch_k(attn_combine_kernel<T>, dim3((unsigned)(nodes * a->H)), dim3(128), 0, s, c);
+  }
+  CSAHCA_CHECK_LAUNCH();
+  return CSAHCA_OK;
+}
+
+int run_tree(const csahca_tree_attn_args* a, void* stream) {
+  int st = validate_tree(a);
+  if (st != CSAHCA_OK) return st;
+  if (a->B == 0 || a->T == 0) return CSAHCA_OK;
+  if ((st = device_ok()) != CSAHCA_OK) return st;
+  const TreeLayout L = tree_layout(a);
+  if (L.tc && (int64_t)a->B * a->T * L.splits * kTcPartialRows > INT32_MAX) return CSAHCA_ERR_UNSUPPORTED;
+  if (!a->workspace || a->workspace_bytes < L.total) return CSAHCA_ERR_WORKSPACE;
+  cudaStream_t s = as_stream(stream);
+  char* ws = static_cast<char*>(a->workspace);
+  return a->dtype == CSAHCA_F32 ? run_tree_t<float>(a, L, ws, s) : run_tree_t<__nv_bfloat16>(a, L, ws, s);
+}
+
 }  // namespace
 
 // ============================================================== C ABI ======
@@ -1319,6 +1756,17 @@ size_t csahca_decode_workspace_size(const csahca_decode_args* args) {
   return decode_layout(args).total;
 }
 
+int qk_norm_rope(const csahca_norm_rope_args* args, void* stream) { return run_norm_rope(args, stream); }
+
+int tree_compress(const csahca_tree_compress_args* args, void* stream) { return run_tree_compress(args, stream); }
+
+int compressed_attn_tree(const csahca_tree_attn_args* args, void* stream) { return run_tree(args, stream); }
+
+size_t csahca_tree_workspace_size(const csahca_tree_attn_args* args) {
+  if (validate_tree(args, true) != CSAHCA_OK || args->B == 0 || args->T == 0) return 0;
+  return tree_layout(args).total;
+}
+
 const char* csahca_status_string(int status) {
   switch (status) {
     case CSAHCA_OK: return "ok";
@@ -1354,6 +1802,9 @@ int64_t csahca_struct_size(int which) {
     case 4: return (int64_t)sizeof(csahca_decode_compress_args);
     case 5: return (int64_t)sizeof(csahca_cp_topk_merge_args);
     case 6: return (int64_t)sizeof(csahca_cp_merge_args);
+    case 7: return (int64_t)sizeof(csahca_norm_rope_args);
+    case 8: return (int64_t)sizeof(csahca_tree_compress_args);
+    case 9: return (int64_t)sizeof(csahca_tree_attn_args);
     default: return -1;
   }
 }

@@ -1,0 +1,192 @@
+// Compressed entries that drafted tokens complete ("Paper Breakdown:
+// DeepSeek-V4", section 4: CSA KV compression, HCA, Additional Techniques).
+//
+// Node i of a draft tree stands at position t = pos[b] + depth.  If t ends a
+// block, (t + 1) % m == 0, the path to the node completes entry
+// (t + 1) / m - 1: per channel the softmax-weighted pool of the block's m
+// tokens (CSA: and of the preceding block's, 2m logits jointly), token p from
+// the path's node at depth p - pos where p >= pos and from the ring of the
+// committed tokens' raw streams otherwise.  Siblings that complete the same
+// entry pool different tokens, so every node has its own row.
+//
+// One CTA = one node; a node that completes nothing leaves at once.  A thread
+// owns a 16-byte vector of channels and every G-th token of the pool, so that
+// all rows of the pool are asked for in one or few round trips to L2 (the call
+// is bound by them, not by its few hundred KB); the G partial softmaxes
+// (max, sum, weighted sum) are joined in shared memory.
+#pragma once
+#include "compress.cuh"
+#include "norm_rope.cuh"
+
+namespace csahca {
+
+constexpr int kTcpThreads = 512;
+constexpr int kTcpMaxTokens = 512;      // 2m (CSA), m (HCA)
+constexpr int kTcpBatch = 4;            // tokens of a thread in flight
+
+template <typename T> constexpr int tree_compress_smem() { return 3 * Vec16<T>::N * kTcpThreads * 4; }
+
+struct TreeCompressParams {
+  const int* parents; const int* pos;
+  const void* nw[4];                    // drafted tokens' streams [B, T, c]: a, b, za, zb (HCA: a, za)
+  const void* ring;                     // [B, R, S, c]
+  const float* bias_a; const float* bias_b; const float* gain;
+  void* out; float* out_scale;          // [B, T, c]; e4m3: codes, [B, T, c / 128]
+  int T, c, m, rms_norm, rope_dims, e4m3;
+  float eps;
+  double theta[kNrMaxPairs];
+};
+
+template <typename T, bool kCSA>
+__global__ void __launch_bounds__(kTcpThreads) tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
+  constexpr int VEC = Vec16<T>::N;
+  constexpr int S = kCSA ? 4 : 2;
+  // partial softmaxes by vector element: thread x's element e at [e][x], conflict-free
+  extern __shared__ __align__(16) float tcp_smem[];
+  float (*st_mx)[kTcpThreads] = reinterpret_cast<float (*)[kTcpThreads]>(tcp_smem);
+  float (*st_s)[kTcpThreads] = st_mx + VEC;
+  float (*st_acc)[kTcpThreads] = st_s + VEC;
+  __shared__ int src_s[kTcpMaxTokens];  // >= 0: node of the tree; < 0: ring slot -1 - src
+  __shared__ int par_s[kTreeMaxNodes], path_s[kTreeMaxNodes], t_s;
+  __shared__ float red_s[kTcpThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tok = blockIdx.x, b = tok / p.T, i = tok - b * p.T;
+  const int t = tree_node(p.parents, p.pos, b, p.T, i, par_s, path_s, &t_s);
+  const int m = p.m, c = p.c;
+  if (t < 0 || (t + 1) % m != 0) return;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int R = kCSA ? 2 * m : m;
+  const int p0 = p.pos[b];
+  const int blk = (t + 1) / m - 1;
+  const int J0 = (kCSA && blk == 0) ? m : 0;          // entry 0 has no preceding block
+  for (int j = J0 + tid; j < R; j += kTcpThreads) {
+    const int q = t + 1 - R + j;                      // token j of the pool (CSA: preceding block first)
+    src_s[j] = q >= p0 ? path_s[q - p0] : -1 - q % R;
+  }
+  __syncthreads();
+
+  const int nv = c / VEC, G = kTcpThreads / nv;       // nv <= 128: G >= 4
+  const int vec = tid % nv, grp = tid / nv, ch0 = vec * VEC;
+  float mx[VEC], s[VEC], acc[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) { mx[e] = -INFINITY; s[e] = 0.f; acc[e] = 0.f; }
+  if (grp < G) {
+    for (int jb = J0 + grp; jb < R; jb += G * kTcpBatch) {
+      uint4 rv[kTcpBatch], rz[kTcpBatch];
+#pragma unroll
+      for (int u = 0; u < kTcpBatch; ++u) {
+        const int j = jb + u * G;
+        if (j < R) {
+          const int sb = (kCSA && j < m) ? 1 : 0;     // CSA: the preceding block reads stream b
+          const int src = src_s[j];
+          const T* rv_p; const T* rz_p;
+          if (src >= 0) {
+            const int64_t o = ((int64_t)b * p.T + src) * c + ch0;
+            rv_p = static_cast<const T*>(p.nw[sb]) + o;
+            rz_p = static_cast<const T*>(p.nw[S / 2 + sb]) + o;
+          } else {
+            const T* ring = static_cast<const T*>(p.ring) + (((int64_t)b * R + (-1 - src)) * S) * c + ch0;
+            rv_p = ring + (int64_t)sb * c;
+            rz_p = ring + (int64_t)(S / 2 + sb) * c;
+          }
+          rv[u] = __ldg(reinterpret_cast<const uint4*>(rv_p));
+          rz[u] = __ldg(reinterpret_cast<const uint4*>(rz_p));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kTcpBatch; ++u) {
+        const int j = jb + u * G;
+        if (j < R) {
+          float v[VEC], z[VEC];
+          unpack16<T>(rv[u], v);
+          unpack16<T>(rz[u], z);
+          const float* bias = kCSA ? (j < m ? p.bias_b + (int64_t)j * c : p.bias_a + (int64_t)(j - m) * c)
+                                   : p.bias_a + (int64_t)j * c;
+#pragma unroll
+          for (int e = 0; e < VEC; e += 4) {
+            const float4 bz = __ldg(reinterpret_cast<const float4*>(bias + ch0 + e));
+            z[e] += bz.x; z[e + 1] += bz.y; z[e + 2] += bz.z; z[e + 3] += bz.w;
+          }
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            if (z[e] != -INFINITY) pool_update(z[e], v[e], mx[e], s[e], acc[e]);   // (weight 0)
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) { st_mx[e][tid] = mx[e]; st_s[e][tid] = s[e]; st_acc[e][tid] = acc[e]; }
+  __syncthreads();
+  // the first nv threads join the groups of their vector
+  float y[VEC];
+  float ss = 0.f;
+  if (tid < nv) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float M = -INFINITY;
+      for (int g = 0; g < G; ++g) M = fmaxf(M, st_mx[e][g * nv + tid]);
+      float sum = 0.f, a = 0.f;
+      for (int g = 0; g < G; ++g) {
+        const float mg = st_mx[e][g * nv + tid];
+        const float f = mg == M ? 1.f : expf(mg - M); // (a group without tokens: expf(-inf) = 0)
+        sum = fmaf(st_s[e][g * nv + tid], f, sum);
+        a = fmaf(st_acc[e][g * nv + tid], f, a);
+      }
+      y[e] = a / sum;
+      ss = fmaf(y[e], y[e], ss);
+    }
+  }
+  if (p.rms_norm) {
+    ss = warp_sum(ss);
+    if (lane == 0) red_s[tid >> 5] = ss;
+    __syncthreads();
+    float tot = 0.f;
+    for (int k = 0; k < (nv + 31) / 32; ++k) tot += red_s[k];
+    const float inv = rsqrtf(tot / (float)c + p.eps);
+    if (tid < nv) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) y[e] *= inv * (p.gain ? __ldg(p.gain + ch0 + e) : 1.f);
+    }
+  }
+  if (tid < nv) {
+    const int j0 = ch0 - (c - p.rope_dims);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      if (j0 + e >= 0) {
+        float cs, sn;
+        rope_sincos((double)blk * (double)m, p.theta[(j0 + e) >> 1], &cs, &sn);
+        const float x0 = y[e], x1 = y[e + 1];
+        y[e] = x0 * cs - x1 * sn;
+        y[e + 1] = x0 * sn + x1 * cs;
+      }
+    }
+  }
+  if (!p.e4m3) {
+    if (tid < nv) store16(static_cast<T*>(p.out) + (int64_t)tok * c + ch0, y);
+    return;
+  }
+  // e4m3 codes with one fp32 scale per 128 channels, amax / 448 (1 for an
+  // all-zero block): the cache's rule, so that a committed key is the same
+  // (nv is a multiple of 128 / VEC lanes, which divides a warp)
+  constexpr int LB = 128 / VEC;
+  if (tid < (nv + 31) / 32 * 32) {
+    float amax = 0.f;
+    if (tid < nv) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[e]));
+    }
+#pragma unroll
+    for (int o = LB / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if (tid < nv) {
+      const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+      uint8_t* o = static_cast<uint8_t*>(p.out) + (int64_t)tok * c + ch0;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        o[e] = __nv_cvt_float_to_fp8(__fdiv_rn(y[e], scale), __NV_SATFINITE, __NV_E4M3);
+      if (ch0 % 128 == 0) p.out_scale[(int64_t)tok * (c / 128) + ch0 / 128] = scale;
+    }
+  }
+}
+
+}  // namespace csahca

@@ -25,11 +25,13 @@ ERR_NO_DEVICE = -7
 
 NOALLOC_SCRATCH_BYTES = 32 << 20    # CSAHCA_NOALLOC_SCRATCH_BYTES
 CP_MAX_RANKS = 64                   # CSAHCA_CP_MAX_RANKS
+TREE_MAX_NODES = 64                 # CSAHCA_TREE_MAX_NODES
 
 F32, BF16, E4M3 = 0, 1, 2
 CSA, HCA = 0, 1
 
 i32, f32, vp, sz = C.c_int32, C.c_float, C.c_void_p, C.c_size_t
+i64 = C.c_int64
 
 
 class CompressArgs(C.Structure):
@@ -90,12 +92,39 @@ class CpMergeArgs(C.Structure):
                 ("partials", vp), ("sinks", vp), ("pos", vp), ("out", vp)]
 
 
+class NormRopeArgs(C.Structure):
+    _fields_ = [("dtype", i32), ("B", i32), ("n", i32), ("HQ", i32), ("HK", i32), ("d", i32),
+                ("rope_dims", i32), ("rope_base", f32), ("eps", f32), ("q_norm", i32),
+                ("k_norm", i32), ("reserved0", i32), ("q_stride", i64 * 3), ("k_stride", i64 * 3),
+                ("q", vp), ("k", vp), ("q_gain", vp), ("k_gain", vp), ("pos", vp), ("q_out", vp),
+                ("k_out", vp)]
+
+
+class TreeCompressArgs(C.Structure):
+    _fields_ = [("kind", i32), ("dtype", i32), ("out_dtype", i32), ("B", i32), ("T", i32), ("c", i32),
+                ("m", i32), ("rms_norm", i32), ("rope_dims", i32), ("rope_base", f32), ("eps", f32),
+                ("reserved0", i32), ("pos", vp), ("parents", vp), ("a", vp), ("b", vp), ("za", vp),
+                ("zb", vp), ("ring", vp), ("bias_a", vp), ("bias_b", vp), ("gain", vp), ("out", vp),
+                ("out_scale", vp)]
+
+
+class TreeAttnArgs(C.Structure):
+    _fields_ = [("kind", i32), ("dtype", i32), ("B", i32), ("T", i32), ("H", i32), ("d", i32),
+                ("N_cap", i32), ("m", i32), ("w", i32), ("k", i32), ("rope_dims", i32),
+                ("rope_base", f32), ("eps", f32), ("scale", f32), ("q_norm", i32), ("kv_norm", i32),
+                ("HI", i32), ("dI", i32), ("qI_dtype", i32), ("kI_dtype", i32),
+                ("q", vp), ("pos", vp), ("parents", vp), ("q_gain", vp), ("kv_gain", vp),
+                ("kv_cache", vp), ("win", vp), ("kv_raw", vp), ("draft", vp), ("sinks", vp), ("qI", vp),
+                ("wI", vp), ("kI", vp), ("kI_scale", vp), ("draft_kI", vp), ("draft_kI_scale", vp),
+                ("idx_in", vp), ("idx_out", vp), ("out", vp), ("workspace", vp), ("workspace_bytes", sz)]
+
+
 class TraceEntry(C.Structure):
     _fields_ = [("name", C.c_char * 48), ("launches", C.c_int64), ("total_ms", C.c_double)]
 
 
 STRUCTS = {0: CompressArgs, 1: IndexerArgs, 2: AttnArgs, 3: DecodeArgs, 4: DecodeCompressArgs,
-           5: CpTopkMergeArgs, 6: CpMergeArgs}
+           5: CpTopkMergeArgs, 6: CpMergeArgs, 7: NormRopeArgs, 8: TreeCompressArgs, 9: TreeAttnArgs}
 
 # Every symbol include/csahca.h declares, with (restype, argtypes).
 SIGNATURES = {
@@ -111,6 +140,10 @@ SIGNATURES = {
     "decode_compress": (C.c_int, [C.POINTER(DecodeCompressArgs), vp]),
     "cp_topk_merge": (C.c_int, [C.POINTER(CpTopkMergeArgs), vp]),
     "cp_attn_merge": (C.c_int, [C.POINTER(CpMergeArgs), vp]),
+    "qk_norm_rope": (C.c_int, [C.POINTER(NormRopeArgs), vp]),
+    "tree_compress": (C.c_int, [C.POINTER(TreeCompressArgs), vp]),
+    "compressed_attn_tree": (C.c_int, [C.POINTER(TreeAttnArgs), vp]),
+    "csahca_tree_workspace_size": (sz, [C.POINTER(TreeAttnArgs)]),
     "csahca_status_string": (C.c_char_p, [C.c_int]),
     "csahca_abi_version": (C.c_int, []),
     "csahca_kv_row_bytes": (C.c_int64, [C.c_int32, C.c_int32, C.c_int32]),
