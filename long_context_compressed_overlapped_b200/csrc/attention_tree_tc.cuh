@@ -4,10 +4,20 @@
 //
 // Both products are written transposed, as in the decode kernel, so that one
 // copy of a key tile serves both (K = V) and O^T [512 x 64] fits TMEM beside
-// S^T:  S^T [128 keys x 64 heads] = K . Q^T,  O^T += V^T . P^T.
+// S^T:  S^T [64 keys x 64 heads] = K . Q^T,  O^T += V^T . P^T.
 //
-// A node's keys are two runs.  Tiles of 128 consecutive committed entries
-// (HCA) arrive by TMA, two 64-dim chunks a box (an SM completes about one TMA
+// The tensor pipe reads its operands from shared memory at 128 bytes a cycle,
+// and at N = 64 that is what an MMA costs: 48 cycles for M = 128, 32 for M = 64
+// (measured; 32 and 16 by arithmetic).  Two key tiles are in flight, so that
+// the scores of tile i + 1 are formed and its successor loads while tile i is
+// in the softmax: tiles of 64 keys (64 KB), since 128 KB of keys fit beside
+// the query.  M = 64 for S^T costs 1,033 + 776 cycles of operand reads a tile
+// (3,620 per 128 keys, against 3,090 with tiles of 128 keys), but one tile of
+// 128 at a time left the pipe idle for the softmax and the load: 7,250 cycles
+// per 128 keys.
+//
+// A node's keys are two runs.  Tiles of 64 consecutive committed entries
+// (HCA) arrive by TMA, four 64-dim chunks a box (an SM completes about one TMA
 // op per 580 cycles whatever its size, so 32 KB boxes).  Everything else is
 // the node's row list, gathered row by row: the selected entries (CSA) or the
 // entries past the last whole tile (HCA), then the plan's list (window rows by
@@ -17,11 +27,12 @@
 // reach O.
 //
 // Roles (896 threads): warps 0-7 softmax and epilogue (two groups of four
-// warps, group g owns heads 32g .. 32g + 31; thread i of a group is key slot i
-// of S^T and dim slot i of each O^T M-tile), warps 8-23 producers, then the
-// S and the P.V MMA issuers.  Each producer warp copies 8 rows of a gathered
-// tile, waits for its own copies of a chunk pair and arrives once (a barrier
-// arrival per lane and chunk was 4,096 of them a tile).
+// warps, group g owns heads 32g .. 32g + 31; S^T is read in the 16 x 256-bit
+// shape, a thread holding two keys of eight heads, with its heads' running
+// maxima and sums in registers), warps 8-23 producers, then the S and the P.V
+// MMA issuers.  Each producer warp copies 4 rows of a gathered tile, waits
+// for its own copies of a half tile and arrives once (a barrier arrival per
+// lane and chunk was 4,096 of them per 128 keys).
 //
 // Work items: (node, split of its tiles).  With one split the item writes the
 // final row, otherwise a partial for tree_combine_kernel.
@@ -33,10 +44,21 @@ namespace csahca {
 
 constexpr int kTreeProducers = 16;
 constexpr int kTreeThreads = 32 * (8 + kTreeProducers + 4);
-constexpr int kTreePairs = kAttnChunks / 2;              // chunk pairs of a tile (= O^T M-tiles)
-static_assert(kTreePairs == kAttnMT, "a chunk pair is one O^T M-tile's rows");
+constexpr int kTreeTile = 64;                            // keys of a tile
+constexpr int kTreeHalfChunks = kAttnChunks / 2;         // a half tile: 4 chunks of 64 dims
+static_assert(kTreeProducers * 4 == kTreeTile, "a producer lane group copies one row of a gathered tile");
+struct TreeSmem {
+  static constexpr int K_CHUNK = kTreeTile * 128;              // 8 KB
+  static constexpr int K_BYTES = kAttnChunks * K_CHUNK;        // 64 KB a tile
+  static constexpr int P_BYTES = kTreeTile * 128;              // 8 KB
+  static constexpr int TOTAL = 1024 + AttnSmem::Q_BYTES + 2 * K_BYTES + 2 * P_BYTES;
+};
 static_assert(256 * kAttnRegsSoftmax + 32 * kTreeProducers * kAttnRegsProducer + 128 * kAttnRegsMma <= 72 * kTreeThreads,
               "the register split fits a 72-register launch");
+
+// Partial of one (node, split): m[H], l[H], O / l [D][H], fp32.
+constexpr int kTreePartialFloats = 2 * kAttnH + kAttnD * kAttnH;
+constexpr int kTreePartialBytes = kTreePartialFloats * 4;
 
 struct TreeAttnParams {
   const __nv_bfloat16* kv;               // [B * N, D]
@@ -50,7 +72,7 @@ struct TreeAttnParams {
   float scale_log2;
   int rope_dims;
   __nv_bfloat16* out;                    // [nodes, H, D]
-  char* partial;                         // [nodes][splits] blocks of kTcPartialBytes
+  char* partial;                         // [nodes][splits] blocks of kTreePartialBytes
   double theta[64];
 };
 
@@ -64,27 +86,30 @@ __device__ __forceinline__ TreeItem tree_item(const TreeAttnParams& p, int id, c
   it.node = id / p.splits;
   it.split = id - it.node * p.splits;
   it.t = f.x;
-  it.full = p.idx ? 0 : f.y >> 7;
-  it.tail = p.idx ? p.k : f.y & 127;
+  it.full = p.idx ? 0 : f.y / kTreeTile;
+  it.tail = p.idx ? p.k : f.y % kTreeTile;
   it.nlist = it.tail + f.z;
-  const int total = f.x < 0 ? 0 : it.full + ((it.nlist + 127) >> 7);
+  const int total = f.x < 0 ? 0 : it.full + (it.nlist + kTreeTile - 1) / kTreeTile;
   it.tile0 = (int)((int64_t)total * it.split / p.splits);
   it.tile1 = (int)((int64_t)total * (it.split + 1) / p.splits);
   return it;
 }
-// Row j of the node's list, or null if it is no key.
-__device__ __forceinline__ const __nv_bfloat16* tree_row(const TreeAttnParams& p, const TreeItem& it, int j) {
-  if (j >= it.nlist) return nullptr;
-  const int b = it.node / p.T;
-  if (j >= it.tail) {
-    const int code = __ldg(p.list + (int64_t)it.node * p.list_stride + (j - it.tail));
-    const int kind = code >> kRowShift;
-    const __nv_bfloat16* base = kind == ROW_RING ? p.rows[0] : kind == ROW_TREE ? p.rows[1] : p.rows[2];
-    return base + (int64_t)(code & kRowMask) * kAttnD;
-  }
-  if (!p.idx) return p.kv + ((int64_t)b * p.N + it.full * 128 + j) * kAttnD;
-  const int e = __ldg(p.idx + (int64_t)it.node * p.k + j);
+// Entry j of the node's list as it stands in memory (the selection's index or
+// the plan's code; asked for a tile ahead), and the row it names, or null if
+// it is no key.
+__device__ __forceinline__ int tree_entry(const TreeAttnParams& p, const TreeItem& it, int j) {
+  if (j >= it.nlist) return -1;
+  if (j >= it.tail) return __ldg(p.list + (int64_t)it.node * p.list_stride + (j - it.tail));
+  return p.idx ? __ldg(p.idx + (int64_t)it.node * p.k + j) : it.full * kTreeTile + j;
+}
+__device__ __forceinline__ const __nv_bfloat16* tree_row(const TreeAttnParams& p, const TreeItem& it, int j, int e) {
   if (e < 0) return nullptr;
+  if (j >= it.tail) {
+    const int kind = e >> kRowShift;
+    const __nv_bfloat16* base = kind == ROW_RING ? p.rows[0] : kind == ROW_TREE ? p.rows[1] : p.rows[2];
+    return base + (int64_t)(e & kRowMask) * kAttnD;
+  }
+  const int b = it.node / p.T;
   if (e < p.N) return p.kv + ((int64_t)b * p.N + e) * kAttnD;
   if (e - p.N < p.T && p.rows[ROW_DRAFT]) return p.rows[ROW_DRAFT] + ((int64_t)b * p.T + (e - p.N)) * kAttnD;
   raise_device_error(DEVERR_BAD_INDEX);
@@ -102,43 +127,82 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst_smem, const void* s
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem),
                "r"(live ? 16 : 0) : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// MMA and commit issued by the elected lane, in code that the whole warp runs:
+// the descriptors stay warp-uniform values (issued from a lane-0 branch, the
+// scalar work around an MMA took 80 to 118 cycles of the pipe's 49).
+__device__ __forceinline__ void umma_bf16_if(uint32_t leader, uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                             uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader));
+}
+__device__ __forceinline__ void umma_commit_if(uint32_t leader, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar)), "r"(leader) : "memory");
+}
+// A converged warp's wait: every lane leaves with the same answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort)) != 0;
+}
+// 16 lanes x 32 columns of 32 bits: thread t gets lanes t / 4 and t / 4 + 8 of
+// columns 8 j + 2 (t % 4) + {0, 1}: v[4 j + {0, 1}] and v[4 j + {2, 3}].
+__device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kTreeThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_constant__ CUtensorMap q_rows,
-                    const __grid_constant__ CUtensorMap part_rows, const __grid_constant__ TreeAttnParams p) {
+                    const __grid_constant__ TreeAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
-  uint8_t* sK = sQ + AttnSmem::Q_BYTES;
-  uint8_t* sP = sK + AttnSmem::K_BYTES;
-  // bar_pv[j]: the tile's P.V MMAs of O^T M-tiles 0 .. j have completed (key
-  // chunk pair j is free; j = 3: O^T and P^T may be touched again)
-  __shared__ uint64_t bar_kfull[kTreePairs], bar_pv[kTreePairs];
-  __shared__ uint64_t bar_q_full, bar_q_empty, bar_s_full, bar_s_empty, bar_p_full, bar_done;
+  uint8_t* sK = sQ + AttnSmem::Q_BYTES;                  // two tiles
+  uint8_t* sP = sK + 2 * TreeSmem::K_BYTES;              // two
+  // Tile n uses buffer n & 1 of keys, S^T and P^T, phase (n >> 1) & 1.
+  // bar_pv[b][h]: the P.V MMAs of the half's two O^T M-tiles have completed (its
+  // four key chunks are free; h = 1: P^T too, and O^T may be touched)
+  __shared__ uint64_t bar_kfull[2][2], bar_pv[2][2], bar_s_full[2], bar_s_free[2], bar_p_full[2];
+  __shared__ uint64_t bar_q_full, bar_q_empty, bar_done;
   __shared__ uint32_t tmem_base_sh;
   __shared__ volatile int abort_flag;
-  __shared__ float red[2][4 * 32];
+  __shared__ __align__(16) float red[2][4][32];
   __shared__ __align__(16) float stat_a[kAttnH];
-  __shared__ __align__(16) float m_use[kAttnH];
-  __shared__ __align__(16) float alpha[kAttnH];
-  __shared__ float l_run[kAttnH];
+  __shared__ float m_run[kAttnH], l_run[kAttnH];
   __shared__ double theta_s[64];
-  __shared__ int need_rescale[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kWarpS = 8 + kTreeProducers, kWarpPV = kWarpS + 1;
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int c = 0; c < kTreePairs; ++c) {
-      mbar_init(&bar_kfull[c], kTreeProducers);
-      mbar_init(&bar_pv[c], 1);
+    for (int x = 0; x < 2; ++x) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&bar_kfull[x][h], kTreeProducers);
+        mbar_init(&bar_pv[x][h], 1);
+      }
+      mbar_init(&bar_s_full[x], 1);
+      mbar_init(&bar_s_free[x], 256);
+      mbar_init(&bar_p_full[x], 256);
     }
     mbar_init(&bar_q_full, 1);
     mbar_init(&bar_q_empty, 1);
-    mbar_init(&bar_s_full, 1);
-    mbar_init(&bar_s_empty, 256);
-    mbar_init(&bar_p_full, 256);
     mbar_init(&bar_done, 2);
     mbar_fence_init();
   }
@@ -148,9 +212,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  const uint32_t tS = tmem;                              // S^T: H columns
+  const uint32_t tS = tmem;                              // S^T of buffer b: columns [64 b, ...), M = 64: keys 16 q ..
+                                                         // 16 q + 15 in lanes 32 q .. 32 q + 15
   const uint32_t tO = tmem + 128;                        // O^T M-tile j: columns [128 + j H, ...)
-  const uint32_t tL = tmem + 128 + kAttnMT * kAttnH;     // per-key-slot sums of p
   // the plan, the finished rows and the selection come from earlier kernels
   griddep_wait();
   griddep_launch_dependents();
@@ -163,8 +227,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
       tma_prefetch_desc(&comp_rows);
       tma_prefetch_desc(&q_rows);
     }
-    const int piece = lane & 7, rg = lane >> 3;
-    const int r0 = 4 * pw + rg, r1 = r0 + 64;            // this lane's rows of a gathered tile
+    const int piece = lane & 7, row = 4 * pw + (lane >> 3);   // this lane's row of a gathered tile
     uint32_t tcount = 0, icount = 0;
     bool stop = false;                                   // warp-uniform
     int4 f = tree_info(p, blockIdx.x);
@@ -185,337 +248,351 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         if (!ok) { stop = true; break; }
         ++icount;
       }
-      const __nv_bfloat16 *n0 = nullptr, *n1 = nullptr;  // the next gathered tile's rows
-      bool have_next = false;
+      // the entry of this lane's row in the next gathered tile
+      int e = tree_entry(p, it, (max(it.tile0, it.full) - it.full) * kTreeTile + row);
       for (int tile = it.tile0; tile < it.tile1 && !stop; ++tile, ++tcount) {
-        const uint32_t ph = tcount & 1;
-        if (tile < it.full) {
-          // 128 consecutive entries: box c (two chunks) by producer warp c
-          const int row0 = (it.node / p.T) * p.N + tile * 128;
-          for (int c = 0; c < kTreePairs; ++c) {
-            int ok = 1;
-            if (lane == 0) {
-              ok = mbar_wait(&bar_pv[c], ph ^ 1, &abort_flag);
-              if (ok) {
-                if (c == pw) {
-                  mbar_expect_tx(&bar_kfull[c], 2 * AttnSmem::K_CHUNK);
-                  tma_load_3d(sK + 2 * c * AttnSmem::K_CHUNK, &comp_rows, 0, row0, 2 * c, &bar_kfull[c]);
-                } else {
-                  mbar_arrive(&bar_kfull[c]);
-                }
+        const int buf = tcount & 1;
+        const uint32_t ph = (tcount >> 1) & 1;
+        uint8_t* dst = sK + buf * TreeSmem::K_BYTES;
+        const bool box = tile < it.full;
+        const int off = (tile - it.full) * kTreeTile;
+        const int fill = box ? 0 : (it.nlist - off + 15) & ~15;   // rows that the P.V MMAs read
+        const __nv_bfloat16* src = nullptr;
+        if (!box) {
+          src = tree_row(p, it, off + row, e);
+          e = tree_entry(p, it, off + kTreeTile + row);
+        }
+        const bool live = src != nullptr;
+        if (!live) src = p.kv;
+        for (int h = 0; h < 2; ++h) {
+          int ok = 1;
+          if (lane == 0) {
+            ok = mbar_wait(&bar_pv[buf][h], ph ^ 1, &abort_flag);
+            if (ok && box) {
+              // 64 consecutive entries: half h (four chunks) by producer warp h
+              if (h == pw) {
+                mbar_expect_tx(&bar_kfull[buf][h], kTreeHalfChunks * TreeSmem::K_CHUNK);
+                tma_load_3d(dst + h * kTreeHalfChunks * TreeSmem::K_CHUNK, &comp_rows, 0,
+                            (it.node / p.T) * p.N + tile * kTreeTile, h * kTreeHalfChunks, &bar_kfull[buf][h]);
+              } else {
+                mbar_arrive(&bar_kfull[buf][h]);
               }
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) { stop = true; break; }
           }
-          continue;
-        }
-        const int off = (tile - it.full) * 128;
-        const int fill = min(128, (it.nlist - off + 15) & ~15);   // rows that the P.V MMAs read
-        const __nv_bfloat16* s0 = have_next ? n0 : tree_row(p, it, off + r0);
-        const __nv_bfloat16* s1 = have_next ? n1 : tree_row(p, it, off + r1);
-        const bool l0 = s0 != nullptr, l1 = s1 != nullptr;
-        if (!l0) s0 = p.kv;
-        if (!l1) s1 = p.kv;
-        for (int c = 0; c < kTreePairs; ++c) {
-          int ok = 1;
-          if (lane == 0) ok = mbar_wait(&bar_pv[c], ph ^ 1, &abort_flag);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) { stop = true; break; }
+          if (!box) {
+            if (row < fill) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint8_t* dst = sK + (2 * c + h) * AttnSmem::K_CHUNK;
-            const int o = (2 * c + h) * 64 + piece * 8;
-            if (r0 < fill) cp_async16_or_zero(dst + sw128_offset(r0, piece * 16), s0 + o, l0);
-            if (r1 < fill) cp_async16_or_zero(dst + sw128_offset(r1, piece * 16), s1 + o, l1);
+              for (int c = 0; c < kTreeHalfChunks; ++c) {
+                const int cc = h * kTreeHalfChunks + c;
+                cp_async16_or_zero(dst + cc * TreeSmem::K_CHUNK + sw128_offset(row, piece * 16),
+                                   src + cc * 64 + piece * 8, live);
+              }
+            }
+            cp_async_commit();
           }
-          cp_async_commit();
         }
-        // the next tile's rows, and their lines into L2 behind this tile's copies
-        have_next = tile + 1 < it.tile1;
-        if (have_next) {
-          n0 = tree_row(p, it, off + 128 + r0);
-          n1 = tree_row(p, it, off + 128 + r1);
-          if (n0) prefetch_l2_line(n0 + piece * 64);
-          if (n1) prefetch_l2_line(n1 + piece * 64);
+        if (box || stop) continue;
+        if (tile + 1 < it.tile1) {
+          // the next tile's lines into L2 behind this tile's copies
+          const __nv_bfloat16* nx = tree_row(p, it, off + kTreeTile + row, e);
+          if (nx) prefetch_l2_line(nx + piece * 64);
         }
-        if (stop) break;
-        // every lane's own copies of pair c have landed and are made visible
+        // every lane's own copies of a half have landed and are made visible
         // to the MMAs (async proxy) before the warp's one arrival
-#pragma unroll
-        for (int c = 0; c < kTreePairs; ++c) {
-          if (c == 0) cp_async_wait<3>();
-          else if (c == 1) cp_async_wait<2>();
-          else if (c == 2) cp_async_wait<1>();
-          else cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_kfull[c]);
-        }
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_kfull[buf][0]);
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_kfull[buf][1]);
       }
     }
     // copies in flight end before the CTA may exit: this lane's gathers here,
     // the boxes and the query by their barriers
     cp_async_wait<0>();
-    if (lane == 0 && pw < kTreePairs && tcount > 0) mbar_wait(&bar_kfull[pw], (tcount - 1) & 1, &abort_flag);
+    if (lane == 0 && pw < 2) {
+      for (uint32_t n = tcount < 2 ? 0 : tcount - 2; n < tcount; ++n)
+        mbar_wait(&bar_kfull[n & 1][pw], (n >> 1) & 1, &abort_flag);
+    }
     if (lane == 0 && pw == 0 && icount > 0) mbar_wait(&bar_q_full, (icount - 1) & 1, &abort_flag);
   } else if (warp >= kWarpS) {
     setmaxnreg_dec<kAttnRegsMma>();
-    if (warp == kWarpS && lane == 0) {
+    if (warp == kWarpS) {
       // ---------------------------------------------------------- S issuer
-      constexpr uint32_t idesc_s = umma_idesc_bf16(128, kAttnH, 0, 0);
+      const uint32_t leader = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kTreeTile, kAttnH, 0, 0);
+      // (descriptors by halves: only the low word, the address, changes)
       const uint64_t kdesc = umma_desc_kmajor(smem_u32(sK)), qdesc = umma_desc_kmajor(smem_u32(sQ));
+      const uint32_t k_lo = (uint32_t)kdesc, k_hi = (uint32_t)(kdesc >> 32);
+      const uint32_t q_lo = (uint32_t)qdesc, q_hi = (uint32_t)(qdesc >> 32);
       uint32_t tcount = 0, icount = 0;
       bool stop = false;
       int4 f = tree_info(p, blockIdx.x);
-      for (int id = blockIdx.x; id < p.n_items && !stop && !abort_flag; id += gridDim.x) {
+      for (int id = blockIdx.x; id < p.n_items && !stop; id += gridDim.x) {
         const TreeItem it = tree_item(p, id, f);
         f = tree_info(p, id + gridDim.x);
         if (it.tile1 <= it.tile0) continue;
-        if (!mbar_wait(&bar_q_full, icount & 1, &abort_flag)) break;
+        if (!mbar_wait_warp(&bar_q_full, icount & 1, &abort_flag)) break;
         ++icount;
         for (int tile = it.tile0; tile < it.tile1 && !stop; ++tile, ++tcount) {
-          const uint32_t ph = tcount & 1;
-          if (!mbar_wait(&bar_s_empty, ph ^ 1, &abort_flag)) { stop = true; break; }
-          tc_fence_after();
-          for (int c = 0; c < kTreePairs; ++c) {
-            if (!mbar_wait(&bar_kfull[c], ph, &abort_flag)) { stop = true; break; }
+          const int buf = tcount & 1;
+          const uint32_t ph = (tcount >> 1) & 1;
+          if (!mbar_wait_warp(&bar_s_free[buf], ph ^ 1, &abort_flag)) { stop = true; break; }
+          const uint32_t kb = k_lo + buf * (TreeSmem::K_BYTES >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!mbar_wait_warp(&bar_kfull[buf][h], ph, &abort_flag)) { stop = true; break; }
             tc_fence_after();
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint64_t kd = kdesc + (uint64_t)((2 * c + h) * (AttnSmem::K_CHUNK >> 4));
-              const uint64_t qd = qdesc + (uint64_t)((2 * c + h) * (AttnSmem::Q_CHUNK >> 4));
+            for (int c = 0; c < kTreeHalfChunks; ++c) {
+              const int cc = h * kTreeHalfChunks + c;
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) umma_bf16(tS, kd + 2 * ks, qd + 2 * ks, idesc_s, (c | h | ks) != 0);
+              for (int ks = 0; ks < 4; ++ks)
+                umma_bf16_if(leader, tS + buf * kAttnH, kb + cc * (TreeSmem::K_CHUNK >> 4) + 2 * ks, k_hi,
+                             q_lo + cc * (AttnSmem::Q_CHUNK >> 4) + 2 * ks, q_hi, idesc_s, (cc | ks) != 0);
             }
           }
           if (stop) break;
-          umma_commit(&bar_s_full);
-          if (tile == it.tile1 - 1) umma_commit(&bar_q_empty);
+          umma_commit_if(leader, &bar_s_full[buf]);
+          if (tile == it.tile1 - 1) umma_commit_if(leader, &bar_q_empty);
         }
       }
-      umma_commit(&bar_done);
-      mbar_wait(&bar_done, 0, &abort_flag);
-    } else if (warp == kWarpPV && lane == 0) {
+      umma_commit_if(leader, &bar_done);
+      mbar_wait_warp(&bar_done, 0, &abort_flag);
+    } else if (warp == kWarpPV) {
       // -------------------------------------------------------- P.V issuer
+      const uint32_t leader = elect_one();
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, kAttnH, 1, 1);
-      const uint64_t vdesc = umma_desc_mnmajor(smem_u32(sK), AttnSmem::K_CHUNK);
-      const uint64_t pdesc = umma_desc_mnmajor(smem_u32(sP), AttnSmem::P_BYTES);
+      const uint64_t vdesc = umma_desc_mnmajor(smem_u32(sK), TreeSmem::K_CHUNK);
+      const uint64_t pdesc = umma_desc_mnmajor(smem_u32(sP), TreeSmem::P_BYTES);
+      const uint32_t v_lo = (uint32_t)vdesc, v_hi = (uint32_t)(vdesc >> 32);
+      const uint32_t p_lo = (uint32_t)pdesc, p_hi = (uint32_t)(pdesc >> 32);
       uint32_t tcount = 0;
       bool stop = false;
       int4 f = tree_info(p, blockIdx.x);
-      for (int id = blockIdx.x; id < p.n_items && !stop && !abort_flag; id += gridDim.x) {
+      for (int id = blockIdx.x; id < p.n_items && !stop; id += gridDim.x) {
         const TreeItem it = tree_item(p, id, f);
         f = tree_info(p, id + gridDim.x);
         for (int tile = it.tile0; tile < it.tile1; ++tile, ++tcount) {
-          if (!mbar_wait(&bar_p_full, tcount & 1, &abort_flag)) { stop = true; break; }
+          const int buf = tcount & 1;
+          if (!mbar_wait_warp(&bar_p_full[buf], (tcount >> 1) & 1, &abort_flag)) { stop = true; break; }
           tc_fence_after();
-          const bool first = tile == it.tile0;
+          const uint32_t first = tile == it.tile0;
           // a list's last tile: P is 0 past its last row, the steps there are skipped
-          const int hi = tile < it.full ? 128 : it.nlist - (tile - it.full) * 128;
-          const int nks = min(8, (hi + 15) >> 4);
+          const int hi = tile < it.full ? kTreeTile : it.nlist - (tile - it.full) * kTreeTile;
+          const int nks = min(kTreeTile / 16, (hi + 15) >> 4);
+          const uint32_t vb = v_lo + buf * (TreeSmem::K_BYTES >> 4), pb = p_lo + buf * (TreeSmem::P_BYTES >> 4);
 #pragma unroll
           for (int mt = 0; mt < kAttnMT; ++mt) {
-            const uint64_t vd = vdesc + (uint64_t)((2 * mt) * (AttnSmem::K_CHUNK >> 4));
-            if (nks == 8) {
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                umma_bf16(tO + mt * kAttnH, vd + 128 * ks, pdesc + 128 * ks, idesc_pv, !(first && ks == 0));
-            } else {
-              for (int ks = 0; ks < nks; ++ks)
-                umma_bf16(tO + mt * kAttnH, vd + 128 * ks, pdesc + 128 * ks, idesc_pv, !(first && ks == 0));
-            }
-            umma_commit(&bar_pv[mt]);
+            for (int ks = 0; ks < kTreeTile / 16; ++ks)
+              if (ks < nks)
+                umma_bf16_if(leader, tO + mt * kAttnH, vb + (2 * mt) * (TreeSmem::K_CHUNK >> 4) + 128 * ks, v_hi,
+                             pb + 128 * ks, p_hi, idesc_pv, ks > 0 || !first);
+            if (mt & 1) umma_commit_if(leader, &bar_pv[buf][mt >> 1]);
           }
         }
       }
-      umma_commit(&bar_done);
-      mbar_wait(&bar_done, 0, &abort_flag);
+      umma_commit_if(leader, &bar_done);
+      mbar_wait_warp(&bar_done, 0, &abort_flag);
     }
   } else {
     setmaxnreg_inc<kAttnRegsSoftmax>();
     // --------------------------------------------------- softmax / epilogue
     const int g = warp >> 2, gid = 1 + g;
-    const int tid = threadIdx.x & 127, st = threadIdx.x;
+    const int tid = threadIdx.x & 127;
     const int h0 = 32 * g;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t tcount = 0;
     const int r0 = kAttnD - p.rope_dims;
-    const float4* mu4 = reinterpret_cast<const float4*>(m_use + h0);
+    const int wq = warp & 3;
+    const int key0 = 16 * wq + (lane >> 2);              // this thread's keys: key0, key0 + 8
+    const int hl = 2 * (lane & 3);                       // its heads: h0 + 8 j + hl + {0, 1}, j = 0 .. 3
     int4 f = tree_info(p, blockIdx.x);
     for (int id = blockIdx.x; id < p.n_items; id += gridDim.x) {
       const TreeItem it = tree_item(p, id, f);
       f = tree_info(p, id + gridDim.x);
       const bool empty = it.tile1 <= it.tile0;
       bool bad = false;                      // uniform over the group; both groups leave together
-      if (tid < 32) m_use[h0 + tid] = -INFINITY;
-      group_sync(gid);
+      float m[8], l[8];                      // [2 j + {0, 1}]: running max (log2 units) and this thread's share of the sum
+#pragma unroll
+      for (int x = 0; x < 8; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
       for (int tile = it.tile0; tile < it.tile1; ++tile, ++tcount) {
         if (bad) continue;
-        const uint32_t ph = tcount & 1;
-        const bool first = tile == it.tile0;
-        const bool valid = tile < it.full || tree_key_valid(p, it, (tile - it.full) * 128 + tid);
-        if (!mbar_wait_group(gid, &bar_s_full, ph, &abort_flag)) { bad = true; continue; }
+        const int buf = tcount & 1;
+        const uint32_t ph = (tcount >> 1) & 1;
+        bool v0 = true, v1 = true;
+        if (tile >= it.full) {
+          v0 = tree_key_valid(p, it, (tile - it.full) * kTreeTile + key0);
+          v1 = tree_key_valid(p, it, (tile - it.full) * kTreeTile + key0 + 8);
+        }
+        if (!mbar_wait_group(gid, &bar_s_full[buf], ph, &abort_flag)) { bad = true; continue; }
         tc_fence_after();
-        float v[32];
-        tmem_ld32(tS + lane_base + h0, v);
+        float v[16];
+        tmem_ld16x256_x4(tS + buf * kAttnH + lane_base + h0, v);
         tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&bar_s_free[buf]);
+        // scaled to log2 units; v[4 j + x]: key 0 for x < 2, key 1 else
+        bool exceed = false;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = valid ? v[e] * p.scale_log2 : -INFINITY;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float sc = (x < 2 ? v0 : v1) ? v[4 * j + x] * p.scale_log2 : -INFINITY;
+            v[4 * j + x] = sc;
+            exceed |= sc > m[2 * j + (x & 1)] + kRescaleThreshold;
+          }
         // the running max is raised only where a score exceeds it by more than
-        // 2^8 (or on the item's first tile)
-        bool exceed = first;
-        if (!first) {
+        // 2^8 (or is the item's first)
+        if (group_any(gid, exceed)) {
+          float t[8];
 #pragma unroll
-          for (int e4 = 0; e4 < 8; ++e4) {
-            const float4 mu = mu4[e4];
-            exceed |= (v[4 * e4 + 0] > mu.x + kRescaleThreshold) | (v[4 * e4 + 1] > mu.y + kRescaleThreshold) |
-                      (v[4 * e4 + 2] > mu.z + kRescaleThreshold) | (v[4 * e4 + 3] > mu.w + kRescaleThreshold);
+          for (int x = 0; x < 8; ++x) {
+            const int j = x >> 1, e = x & 1;
+            t[x] = fmaxf(v[4 * j + e], v[4 * j + 2 + e]);
+            t[x] = fmaxf(t[x], __shfl_xor_sync(0xffffffffu, t[x], 4));
+            t[x] = fmaxf(t[x], __shfl_xor_sync(0xffffffffu, t[x], 8));
+            t[x] = fmaxf(t[x], __shfl_xor_sync(0xffffffffu, t[x], 16));
           }
-        }
-        exceed = group_any(gid, exceed);
-        bool rescale = false;
-        if (exceed) {
-          {
-            float x[32];
+          if (lane < 4) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = v[e];
-            reduce_group32<true>(x, red[g], stat_a + h0, gid);
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float2*>(&red[g][wq][8 * j + hl]) = make_float2(t[2 * j], t[2 * j + 1]);
           }
-          if (tid == 0) need_rescale[g] = 0;
           group_sync(gid);
-          if (tid < 32) {
-            const int h = h0 + tid;
-            const float mt = stat_a[h], mo = m_use[h];
-            float a = 1.f;
-            if (mt > mo + kRescaleThreshold || (mo == -INFINITY && mt != -INFINITY)) {
-              a = (mo == -INFINITY) ? 0.f : exp2f(mo - mt);
-              m_use[h] = mt;
-              if (!first) need_rescale[g] = 1;
+          bool rescale = false;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 mt = *reinterpret_cast<const float2*>(&red[g][0][8 * j + hl]);
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+              const float2 o = *reinterpret_cast<const float2*>(&red[g][w][8 * j + hl]);
+              mt.x = fmaxf(mt.x, o.x);
+              mt.y = fmaxf(mt.y, o.y);
             }
-            alpha[h] = a;
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float tm = e ? mt.y : mt.x, mo = m[2 * j + e];
+              al[e] = 1.f;
+              if (tm > mo + kRescaleThreshold) {          // (true of any score while mo = -inf)
+                al[e] = mo == -INFINITY ? 0.f : exp2f(mo - tm);
+                m[2 * j + e] = tm;
+                rescale |= mo != -INFINITY;
+              }
+              l[2 * j + e] *= al[e];
+            }
+            if (wq == 0 && lane < 4) *reinterpret_cast<float2*>(&stat_a[h0 + 8 * j + hl]) = make_float2(al[0], al[1]);
           }
-          group_sync(gid);
-          rescale = need_rescale[g] != 0;
-        }
-        // the previous tile's P.V has finished: P^T may be overwritten and
-        // O^T / the sums rescaled
-        if (!first) {
-          if (!mbar_wait_group(gid, &bar_pv[kAttnMT - 1], ph ^ 1, &abort_flag)) { bad = true; continue; }
-          tc_fence_after();
-        }
-        if (rescale) {
-          const float4* al4 = reinterpret_cast<const float4*>(alpha + h0);
+          // O^T is rescaled where a head had keys already, once the P.V of the
+          // tile before has completed (the barrier also publishes stat_a)
+          if (group_any(gid, rescale)) {
+            const uint32_t n = tcount - 1;               // (a head with keys: not the item's first tile)
+            if (!mbar_wait_group(gid, &bar_pv[n & 1][1], (n >> 1) & 1, &abort_flag)) { bad = true; continue; }
+            tc_fence_after();
+            const float4* al4 = reinterpret_cast<const float4*>(stat_a + h0);
 #pragma unroll 1
-          for (int mt = 0; mt <= kAttnMT; ++mt) {
-            float o[32];
-            const uint32_t a = (mt < kAttnMT ? tO + mt * kAttnH : tL) + lane_base + h0;
-            tmem_ld32(a, o);
-            tmem_wait_ld();
+            for (int mt = 0; mt < kAttnMT; ++mt) {
+              float o[32];
+              const uint32_t a = tO + mt * kAttnH + lane_base + h0;
+              tmem_ld32(a, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e4 = 0; e4 < 8; ++e4) {
-              const float4 al = al4[e4];
-              o[4 * e4 + 0] *= al.x; o[4 * e4 + 1] *= al.y; o[4 * e4 + 2] *= al.z; o[4 * e4 + 3] *= al.w;
+              for (int e4 = 0; e4 < 8; ++e4) {
+                const float4 al = al4[e4];
+                o[4 * e4 + 0] *= al.x; o[4 * e4 + 1] *= al.y; o[4 * e4 + 2] *= al.z; o[4 * e4 + 3] *= al.w;
+              }
+              tmem_st32(a, o);
             }
-            tmem_st32(a, o);
+            tmem_wait_st();
+            tc_fence_before();
           }
-          tmem_wait_st();
         }
-        // p = 2^(s - m), 0 for a key slot that is no key
-#pragma unroll
-        for (int e4 = 0; e4 < 8; ++e4) {
-          const float4 mu = mu4[e4];
-          v[4 * e4 + 0] = valid ? fast_exp2(v[4 * e4 + 0] - mu.x) : 0.f;
-          v[4 * e4 + 1] = valid ? fast_exp2(v[4 * e4 + 1] - mu.y) : 0.f;
-          v[4 * e4 + 2] = valid ? fast_exp2(v[4 * e4 + 2] - mu.z) : 0.f;
-          v[4 * e4 + 3] = valid ? fast_exp2(v[4 * e4 + 3] - mu.w) : 0.f;
-        }
+        // P^T buffer free: the P.V of the tile before the last has completed
+        if (tcount >= 2 && !mbar_wait_group(gid, &bar_pv[buf][1], ph ^ 1, &abort_flag)) { bad = true; continue; }
+        // p = 2^(s - m), 0 for a key slot that is no key (m = -inf: no key yet)
+        uint8_t* P = sP + buf * TreeSmem::P_BYTES;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint4 o;
-          store16(reinterpret_cast<__nv_bfloat16*>(&o), v + 8 * j);
-          *reinterpret_cast<uint4*>(sP + sw128_offset(tid, (4 * g + j) * 16)) = o;
-        }
-        {
-          const uint32_t la = tL + lane_base + h0;
-          if (!first) {
-            float l[32];
-            tmem_ld32(la, l);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] += l[e];
-          }
-          tmem_st32(la, v);
-          tmem_wait_st();
+          const float ma = m[2 * j] == -INFINITY ? 0.f : m[2 * j], mb = m[2 * j + 1] == -INFINITY ? 0.f : m[2 * j + 1];
+          const float p0 = fast_exp2(v[4 * j] - ma), p1 = fast_exp2(v[4 * j + 1] - mb);
+          const float p2 = fast_exp2(v[4 * j + 2] - ma), p3 = fast_exp2(v[4 * j + 3] - mb);
+          l[2 * j] += p0 + p2;
+          l[2 * j + 1] += p1 + p3;
+          const uint32_t piece = (4 * g + j) * 16;
+          *reinterpret_cast<uint32_t*>(P + sw128_offset(key0, piece) + 2 * hl) = pack_bf16x2(p0, p1);
+          *reinterpret_cast<uint32_t*>(P + sw128_offset(key0 + 8, piece) + 2 * hl) = pack_bf16x2(p2, p3);
         }
         fence_proxy_async_smem();
-        tc_fence_before();
-        mbar_arrive(&bar_s_empty);
-        mbar_arrive(&bar_p_full);
+        mbar_arrive(&bar_p_full[buf]);
       }
       // ---- epilogue
       if (!empty && !bad) {
-        if (!mbar_wait_group(gid, &bar_pv[kAttnMT - 1], (tcount - 1) & 1, &abort_flag)) bad = true;
+        const uint32_t n = tcount - 1;
+        if (!mbar_wait_group(gid, &bar_pv[n & 1][1], (n >> 1) & 1, &abort_flag)) bad = true;
         else tc_fence_after();
       }
       if (!empty && !bad) {
-        float v[32];
-        tmem_ld32(tL + lane_base + h0, v);
-        tmem_wait_ld();
-        reduce_group32<false>(v, red[g], l_run + h0, gid);
+        // the group's 64 key slots' sums
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 4);
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 8);
+          l[x] += __shfl_xor_sync(0xffffffffu, l[x], 16);
+        }
+        if (lane < 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<float2*>(&red[g][wq][8 * j + hl]) = make_float2(l[2 * j], l[2 * j + 1]);
+            if (wq == 0) { m_run[h0 + 8 * j + hl] = m[2 * j]; m_run[h0 + 8 * j + hl + 1] = m[2 * j + 1]; }
+          }
+        }
+        group_sync(gid);
+        if (tid < 32) l_run[h0 + tid] = red[g][0][tid] + red[g][1][tid] + red[g][2][tid] + red[g][3][tid];
       }
       bad = softmax_any256(bad);
       if (!bad && it.t >= 0) {
         if (p.splits > 1) {
-          // m[H] (log2 units) and l[H] in fp32, then O / l as bf16 [D][H]; a
-          // split without keys writes its header only (m = -inf, l = 0)
-          float* hdr = reinterpret_cast<float*>(p.partial + (int64_t)id * kTcPartialBytes);
+          // m[H] (log2 units), l[H] and O / l [D][H], all fp32 (a node's splits
+          // are joined without a rounding in between); a split without keys
+          // writes its header only (m = -inf, l = 0)
+          float* blk = reinterpret_cast<float*>(p.partial + (int64_t)id * kTreePartialBytes);
           if (tid < 32) {
             const int h = h0 + tid;
             const float l = empty ? 0.f : l_run[h];
-            hdr[h] = l > 0.f ? m_use[h] : -INFINITY;
-            hdr[kAttnH + h] = l;
+            blk[h] = l > 0.f ? m_run[h] : -INFINITY;
+            blk[kAttnH + h] = l;
             stat_a[h] = l > 0.f ? 1.f / l : 0.f;
           }
           group_sync(gid);
           if (!empty) {
             const float4* f4 = reinterpret_cast<const float4*>(stat_a + h0);
-            const bool own_k = p.n_items <= (int)gridDim.x;   // the CTA's only item: stage in the key buffer
 #pragma unroll 1
             for (int mt = 0; mt < kAttnMT; ++mt) {
-              uint8_t* stg = own_k ? sK + mt * AttnSmem::K_CHUNK : sP;
               float o[32];
               tmem_ld32(tO + lane_base + mt * kAttnH + h0, o);
               tmem_wait_ld();
+              // this thread's dim, the group's 32 heads: 128 contiguous bytes
+              float4* dst = reinterpret_cast<float4*>(blk + 2 * kAttnH + (mt * 128 + tid) * kAttnH + h0);
 #pragma unroll
               for (int e4 = 0; e4 < 8; ++e4) {
                 const float4 fc = f4[e4];
-                o[4 * e4 + 0] *= fc.x; o[4 * e4 + 1] *= fc.y; o[4 * e4 + 2] *= fc.z; o[4 * e4 + 3] *= fc.w;
+                dst[e4] = make_float4(o[4 * e4] * fc.x, o[4 * e4 + 1] * fc.y, o[4 * e4 + 2] * fc.z, o[4 * e4 + 3] * fc.w);
               }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint4 w;
-                store16(reinterpret_cast<__nv_bfloat16*>(&w), o + 8 * q);
-                *reinterpret_cast<uint4*>(stg + sw128_offset(tid, (4 * g + q) * 16)) = w;
-              }
-              fence_proxy_async_smem();
-              softmax_sync256();
-              if (st == 0) {
-                tma_store_2d(&part_rows, stg, 0, id * kTcPartialRows + kTcPartialHeaderRows + mt * 128);
-                bulk_commit();
-                if (!own_k) bulk_wait_read<0>();
-              }
-              if (!own_k) softmax_sync256();
             }
-            if (st == 0) bulk_wait_read<0>();
           }
         } else {
           // o = O / (l + e^{z - m}), rope dims rotated back by -t
           __nv_bfloat16* O = p.out + (int64_t)it.node * kAttnH * kAttnD;
-          if (tid < 32) {
+          if (tid < 32) {                    // (this warp wrote l_run; m_run: see the barrier above)
             const int h = h0 + tid;
             const float z2 = p.sinks[h] * kLog2e;
-            const float mu = empty ? -INFINITY : m_use[h];
+            const float mu = empty ? -INFINITY : m_run[h];
             const float M = fmaxf(mu, z2);
             const float den = exp2f(z2 - M) + (mu == -INFINITY ? 0.f : l_run[h] * exp2f(mu - M));
             // no key, or all weight on an infinite sink: o = 0
@@ -578,9 +655,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
 // ---------------------------------------------------------------------------
 // Join of a node's splits with the sink, and the output de-rotation:
 // o = sum_s f_s (O_s / l_s), f_s = l_s 2^(m_s - M) / (2^(z - M) + sum_s l_s 2^(m_s - M)).
-// One CTA per (node, 64 dims).  The partials are in L2; each thread reads its
-// dim pair's 8 heads of four splits at a time, so the kernel is two or three
+// One CTA per (node, 32 dims).  The partials are in L2; each thread reads its
+// dim pair's 4 heads of four splits at a time, so the kernel is two or three
 // L2 round trips.
+constexpr int kTreeCombineDims = 32;
 constexpr int kTreeCombineThreads = 256;
 constexpr int kTreeMaxSplits = 148;
 
@@ -592,23 +670,23 @@ struct TreeCombineParams {
 };
 
 __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const __grid_constant__ TreeCombineParams p) {
-  __shared__ float w_s[kTreeMaxSplits][kAttnH];
-  __shared__ __align__(16) __nv_bfloat16 stage[kAttnH][64 + 8];
+  __shared__ __align__(16) float w_s[kTreeMaxSplits][kAttnH];
+  __shared__ __align__(16) __nv_bfloat16 stage[kAttnH][kTreeCombineDims + 8];
   __shared__ float red[4][kAttnH];
   griddep_wait();
   griddep_launch_dependents();
-  const int node = blockIdx.x, d0 = blockIdx.y * 64;
+  const int node = blockIdx.x, d0 = blockIdx.y * kTreeCombineDims;
   const int t = p.node_pos[node];
   if (t < 0) return;
   const int tid = threadIdx.x;
-  const char* P = p.partial + (int64_t)node * p.splits * kTcPartialBytes;
+  const float* P = reinterpret_cast<const float*>(p.partial) + (int64_t)node * p.splits * kTreePartialFloats;
   // weights: thread (head h, part) takes the splits part, part + 4, ...
   {
     const int h = tid & 63, part = tid >> 6;
     const float z2 = p.sinks[h] * kLog2e;
     float mx = -INFINITY;
     for (int s = part; s < p.splits; s += 4) {
-      const float m = *reinterpret_cast<const float*>(P + (int64_t)s * kTcPartialBytes + h * 4);
+      const float m = P[(int64_t)s * kTreePartialFloats + h];
       w_s[s][h] = m;
       mx = fmaxf(mx, m);
     }
@@ -619,8 +697,7 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
     float den = 0.f;
     for (int s = part; s < p.splits; s += 4) {
       const float m = w_s[s][h];
-      const float f = m == -INFINITY ? 0.f
-                      : *reinterpret_cast<const float*>(P + (int64_t)s * kTcPartialBytes + (kAttnH + h) * 4) * exp2f(m - M);
+      const float f = m == -INFINITY ? 0.f : P[(int64_t)s * kTreePartialFloats + kAttnH + h] * exp2f(m - M);
       w_s[s][h] = f;
       den += f;
     }
@@ -636,32 +713,29 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
     }
   }
   __syncthreads();
-  const int dp = tid >> 3, hg = tid & 7;                 // dims d0 + 2 dp, + 1; heads 8 hg ..
-  const char* src = P + kTcPartialHeader + ((int64_t)(d0 + 2 * dp) * kAttnH + 8 * hg) * 2;
-  float a0[8], a1[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) { a0[e] = 0.f; a1[e] = 0.f; }
+  const int dp = tid >> 4, h4 = (tid & 15) * 4;          // dims d0 + 2 dp, + 1; heads h4 .. h4 + 3
+  const float* src = P + 2 * kAttnH + (d0 + 2 * dp) * kAttnH + h4;
+  float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < p.splits; s0 += 4) {
-    uint4 x[4], y[4];
+    float4 x[4], y[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (s0 + u < p.splits) {
-        x[u] = *reinterpret_cast<const uint4*>(src + (int64_t)(s0 + u) * kTcPartialBytes);
-        y[u] = *reinterpret_cast<const uint4*>(src + (int64_t)(s0 + u) * kTcPartialBytes + kAttnH * 2);
+        x[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats);
+        y[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats + kAttnH);
       }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (s0 + u < p.splits) {
-        float f0[8], f1[8];
-        unpack16<__nv_bfloat16>(x[u], f0);
-        unpack16<__nv_bfloat16>(y[u], f1);
+        const float4 w = *reinterpret_cast<const float4*>(&w_s[s0 + u][h4]);
+        const float ws[4] = {w.x, w.y, w.z, w.w};
+        const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float w = w_s[s0 + u][8 * hg + e];
+        for (int e = 0; e < 4; ++e) {
           // (a split of weight 0 may hold no O: its bytes are not used)
-          a0[e] += w != 0.f ? w * f0[e] : 0.f;
-          a1[e] += w != 0.f ? w * f1[e] : 0.f;
+          a0[e] += ws[e] != 0.f ? ws[e] * xs[e] : 0.f;
+          a1[e] += ws[e] != 0.f ? ws[e] * ys[e] : 0.f;
         }
       }
     }
@@ -671,22 +745,19 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
     float cs, sn;
     rope_sincos(-(double)t, p.theta[j0 >> 1], &cs, &sn);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
       const float x0 = a0[e], x1 = a1[e];
       a0[e] = x0 * cs - x1 * sn;
       a1[e] = x0 * sn + x1 * cs;
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    *reinterpret_cast<__nv_bfloat162*>(&stage[8 * hg + e][2 * dp]) = __floats2bfloat162_rn(a0[e], a1[e]);
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<__nv_bfloat162*>(&stage[h4 + e][2 * dp]) = __floats2bfloat162_rn(a0[e], a1[e]);
   __syncthreads();
-  __nv_bfloat16* O = p.out + (int64_t)node * kAttnH * kAttnD + d0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int x = tid + 256 * i, h = x >> 3, pc = (x & 7) * 8;
-    *reinterpret_cast<uint4*>(O + (int64_t)h * kAttnD + pc) = *reinterpret_cast<const uint4*>(&stage[h][pc]);
-  }
+  const int h = tid >> 2, pc = (tid & 3) * 8;
+  *reinterpret_cast<uint4*>(p.out + ((int64_t)node * kAttnH + h) * kAttnD + d0 + pc) =
+      *reinterpret_cast<const uint4*>(&stage[h][pc]);
 }
 
 }  // namespace csahca

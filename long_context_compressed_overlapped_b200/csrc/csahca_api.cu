@@ -1511,10 +1511,10 @@ TreeLayout tree_layout(const csahca_tree_attn_args* a) {
   const int64_t jmax = (csa ? (int64_t)a->k : (int64_t)a->N_cap) + a->w + (csa ? 0 : a->T);
   L.keys_per_split = 0;
   if (L.tc) {
-    const int64_t tiles = csa ? ceil_div64((int64_t)a->k + a->w, 128)
-                              : a->N_cap / 128 + ceil_div64((int64_t)(a->N_cap & 127) + a->w, 128);
+    const int64_t tiles = csa ? ceil_div64((int64_t)a->k + a->w, kTreeTile)
+                              : a->N_cap / kTreeTile + ceil_div64((int64_t)(a->N_cap % kTreeTile) + a->w, kTreeTile);
     L.splits = tree_splits(nodes, (int)(tiles > 0 ? tiles : 1));
-    L.partial = L.splits > 1 ? take((size_t)nodes * L.splits * kTcPartialBytes) : off;
+    L.partial = L.splits > 1 ? take((size_t)nodes * L.splits * kTreePartialBytes) : off;
   } else {
     const int64_t ctas = nodes * ceil_div64(a->H, kSimtHG);
     int64_t s = ceil_div64(4 * num_sms(), ctas > 0 ? ctas : 1);
@@ -1544,25 +1544,20 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   p.splits = L.splits; p.n_items = nodes * L.splits; p.scale_log2 = scale * kLog2e; p.rope_dims = a->rope_dims;
   p.out = static_cast<__nv_bfloat16*>(a->out); p.partial = ws + L.partial;
   rope_theta_table(p.theta, a->rope_dims, base);
-  // rows of 512 bf16 as [chunk 8][row][64]: a key box is two chunks of 128
+  // rows of 512 bf16 as [chunk 8][row][64]: a key box is four chunks of 64
   // rows (32 KB), the query box all 8 chunks of a node's 64 heads
-  CUtensorMap m_rows, m_q, m_part;
+  CUtensorMap m_rows, m_q;
   const uint64_t rs = kAttnD * 2;
   if (!encode_3d(&m_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, 64, (uint64_t)nodes * kAttnH, kAttnChunks, rs, 128, 64,
                  kAttnH, kAttnChunks, CU_TENSOR_MAP_SWIZZLE_128B))
     return CSAHCA_ERR_LAUNCH;
   m_rows = m_q;
-  m_part = m_q;
   const uint64_t comp_rows = (uint64_t)a->B * a->N_cap;
-  if (!sel && comp_rows >= 128 &&
-      !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->kv_cache, 64, comp_rows, kAttnChunks, rs, 128, 64, 128,
-                 2, CU_TENSOR_MAP_SWIZZLE_128B))
+  if (!sel && comp_rows >= kTreeTile &&
+      !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->kv_cache, 64, comp_rows, kAttnChunks, rs, 128, 64,
+                 kTreeTile, kTreeHalfChunks, CU_TENSOR_MAP_SWIZZLE_128B))
     return CSAHCA_ERR_LAUNCH;
-  if (L.splits > 1 &&
-      !encode_2d(&m_part, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.partial, kAttnH, (uint64_t)p.n_items * kTcPartialRows,
-                 kAttnH, 128, CU_TENSOR_MAP_SWIZZLE_128B))
-    return CSAHCA_ERR_LAUNCH;
-  cudaFuncSetAttribute(attn_tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AttnSmem::TOTAL);
+  cudaFuncSetAttribute(attn_tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem::TOTAL);
   // the register split must fit the launch allocation (an increase would wait)
   static int launch_regs = -1;
   if (launch_regs < 0) {
@@ -1575,7 +1570,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   const int grid = p.n_items < num_sms() ? p.n_items : num_sms();
   {
     CSAHCA_TRACE(sel ? "attn_tree_csa_tc" : "attn_tree_hca_tc", s);
-    launch_k(attn_tree_tc_kernel, dim3((unsigned)grid), dim3(kTreeThreads), AttnSmem::TOTAL, s, m_rows, m_q, m_part, p);
+    launch_k(attn_tree_tc_kernel, dim3((unsigned)grid), dim3(kTreeThreads), TreeSmem::TOTAL, s, m_rows, m_q, p);
   }
   CSAHCA_CHECK_LAUNCH();
   if (L.splits > 1) {
@@ -1585,7 +1580,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     c.out = p.out; c.splits = L.splits; c.rope_dims = a->rope_dims;
     memcpy(c.theta, p.theta, sizeof(c.theta));
     CSAHCA_TRACE("attn_tree_combine", s);
-    launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / 64), dim3(kTreeCombineThreads), 0, s, c);
+    launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / kTreeCombineDims), dim3(kTreeCombineThreads), 0, s, c);
     CSAHCA_CHECK_LAUNCH();
   }
   return CSAHCA_OK;
@@ -1692,7 +1687,7 @@ int run_tree(const csahca_tree_attn_args* a, void* stream) {
   if (a->B == 0 || a->T == 0) return CSAHCA_OK;
   if ((st = device_ok()) != CSAHCA_OK) return st;
   const TreeLayout L = tree_layout(a);
-  if (L.tc && (int64_t)a->B * a->T * L.splits * kTcPartialRows > INT32_MAX) return CSAHCA_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * a->T * L.splits > INT32_MAX) return CSAHCA_ERR_UNSUPPORTED;
   if (!a->workspace || a->workspace_bytes < L.total) return CSAHCA_ERR_WORKSPACE;
   cudaStream_t s = as_stream(stream);
   char* ws = static_cast<char*>(a->workspace);
