@@ -294,11 +294,6 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
           }
         }
         if (box || stop) continue;
-        if (tile + 1 < it.tile1) {
-          // the next tile's lines into L2 behind this tile's copies
-          const __nv_bfloat16* nx = tree_row(p, it, off + kTreeTile + row, e);
-          if (nx) prefetch_l2_line(nx + piece * 64);
-        }
         // every lane's own copies of a half have landed and are made visible
         // to the MMAs (async proxy) before the warp's one arrival
         cp_async_wait<1>();
@@ -309,6 +304,11 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_kfull[buf][1]);
+        if (tile + 1 < it.tile1) {
+          // the next tile's lines into L2, while its buffer is still in use
+          const __nv_bfloat16* nx = tree_row(p, it, off + kTreeTile + row, e);
+          if (nx) prefetch_l2_line(nx + piece * 64);
+        }
       }
     }
     // copies in flight end before the CTA may exit: this lane's gathers here,
@@ -430,7 +430,9 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
           v0 = tree_key_valid(p, it, (tile - it.full) * kTreeTile + key0);
           v1 = tree_key_valid(p, it, (tile - it.full) * kTreeTile + key0 + 8);
         }
-        if (!mbar_wait_group(gid, &bar_s_full[buf], ph, &abort_flag)) { bad = true; continue; }
+        // (a wait that gives up is settled with the vote below: until then its
+        // threads work on what the buffers hold)
+        const bool ok = mbar_wait(&bar_s_full[buf], ph, &abort_flag);
         tc_fence_after();
         float v[16];
         tmem_ld16x256_x4(tS + buf * kAttnH + lane_base + h0, v);
@@ -438,7 +440,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         tc_fence_before();
         mbar_arrive(&bar_s_free[buf]);
         // scaled to log2 units; v[4 j + x]: key 0 for x < 2, key 1 else
-        bool exceed = false;
+        bool exceed = !ok;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -450,6 +452,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         // the running max is raised only where a score exceeds it by more than
         // 2^8 (or is the item's first)
         if (group_any(gid, exceed)) {
+          if (!group_all(gid, ok)) { bad = true; continue; }
           float t[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
@@ -513,8 +516,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
             tc_fence_before();
           }
         }
-        // P^T buffer free: the P.V of the tile before the last has completed
-        if (tcount >= 2 && !mbar_wait_group(gid, &bar_pv[buf][1], ph ^ 1, &abort_flag)) { bad = true; continue; }
+        // (the P^T buffer is free: these scores' keys were loaded once the P.V of
+        // the tile before the last had completed)
         // p = 2^(s - m), 0 for a key slot that is no key (m = -inf: no key yet)
         uint8_t* P = sP + buf * TreeSmem::P_BYTES;
 #pragma unroll
