@@ -1275,17 +1275,31 @@ void rope_theta_pairs(double* theta, int r, double base) {
 
 template <typename T, int LPR, int NCH, bool kTree>
 void launch_norm_rope_t(NormRopeParams& p, int64_t tokens, cudaStream_t s) {
-  // about four CTAs an SM or a whole token a CTA, whichever is fewer CTAs
-  constexpr int RPC = kNrThreads / LPR;
+  // a token's rows over as many CTAs as fill the SMs four times, or, where it
+  // has few, tokens together up to two turns of a CTA and its table of angles
+  constexpr int RPC = kNrThreads / LPR, kTurn = (NCH >= 2 ? 2 : 4) * RPC;
   const int rows = p.heads[0] + p.heads[1];
-  int64_t groups = ceil_div64(4 * num_sms(), tokens);
+  const int64_t want = 4 * num_sms();
+  p.tokens = (int)tokens;
+  p.tpc = 1;
+  if (!kTree && rows < 2 * kTurn && tokens > want) {
+    int64_t t = 2 * kTurn / rows;
+    if (p.rope_dims > 0 && t > kNrTable / (p.rope_dims / 2)) t = kNrTable / (p.rope_dims / 2);
+    if (t > tokens / want) t = tokens / want;
+    if (t > kNrMaxTokens) t = kNrMaxTokens;
+    if (t > 1) p.tpc = (int)t;
+  }
+  int64_t groups = ceil_div64(want, tokens);
   const int64_t most = ceil_div64(rows, RPC);
   if (groups > most) groups = most;
-  if (groups < 1) groups = 1;
+  if (groups < 1 || p.tpc > 1) groups = 1;
   p.rows_per_cta = (int)(ceil_div64(ceil_div64(rows, groups), RPC) * RPC);
-  groups = rows > 0 ? ceil_div64(rows, p.rows_per_cta) : 1;
+  groups = rows > 0 && p.tpc == 1 ? ceil_div64(rows, p.rows_per_cta) : 1;
   CSAHCA_TRACE(kTree ? "tree_norm_rope" : "qk_norm_rope", s);
-  launch_k(norm_rope_kernel<T, LPR, NCH, kTree>, dim3((unsigned)tokens, (unsigned)groups), dim3(kNrThreads), 0, s, p);
+  p.inv_d = 1.0f / (float)p.d;
+  const dim3 grid((unsigned)ceil_div64(tokens, p.tpc), (unsigned)groups);
+  if (p.d == LPR * NCH * Vec16<T>::N) launch_k(norm_rope_kernel<T, LPR, NCH, true, kTree>, grid, dim3(kNrThreads), 0, s, p);
+  else launch_k(norm_rope_kernel<T, LPR, NCH, false, kTree>, grid, dim3(kNrThreads), 0, s, p);
 }
 
 template <typename T, bool kTree>

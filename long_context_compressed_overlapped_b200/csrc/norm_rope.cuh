@@ -4,14 +4,17 @@
 //
 //   y = RoPE_pos(x / sqrt(mean(x^2) + eps) * gain), the last r dims rotated.
 //
-// One CTA = one token x a run of its heads.  The rows go through registers
-// once (read, summed, scaled, rotated, written: 2 d e bytes a row, so HBM is
-// the bound); the token's r/2 rotation angles are the same for every head, so
-// the CTA forms them once, in double, while its first rows are in flight.
-// LPR lanes share a row (a power of two, so that a row of 64 bf16 dims takes 8
-// lanes and a warp 4 rows), each with NCH 16-byte pieces; a lane keeps the
-// pieces of up to four rows in flight, packed.  Arithmetic is fp32 and the one
-// rounding is the store's.
+// The rows go through registers once (read, summed, scaled, rotated, written:
+// 2 d e bytes a row, so HBM is the bound).  One CTA = one token x a run of its
+// heads, or several tokens where a token has few (a CTA per token of 5 rows of
+// 64 dims left HBM at 780 GB/s).  A token's r/2 rotation angles are the same for
+// every head, so the CTA forms them once, in double, while its first rows are
+// in flight.  LPR lanes share a row (a power of two, so that a row of 64 bf16
+// dims takes 8 lanes and a warp 4 rows), each with NCH 16-byte pieces; a lane
+// keeps the pieces of two or four rows in flight, packed, and 64 registers a
+// thread let 32 warps an SM overlap.  bf16 rows are bound by instructions
+// before HBM: the arithmetic is in pairs (two fp32 lanes an instruction).
+// Arithmetic is fp32 and the one rounding is the store's.
 //
 // kTree: the tokens are the nodes of draft trees.  A node's position is pos[b]
 // plus its depth, found by walking its parents; the CTA of a node's first
@@ -23,6 +26,8 @@ namespace csahca {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrMaxPairs = 256;       // rope dims <= 512
+constexpr int kNrTable = 512;          // angles of a CTA: its tokens x r / 2
+constexpr int kNrMaxTokens = 64;       // tokens of a CTA
 constexpr int kTreeMaxNodes = 64;
 
 // Row codes of a node's own key list: window rows by position, then (HCA) the
@@ -48,8 +53,9 @@ struct NormRopeParams {
   int64_t xs[2][3], ys[2][3];           // element strides of batch, token, head
   int heads[2], norm[2];
   const int* pos;                       // [B, n]; < 0: the token's rows are left as they are
-  int n, d, rope_dims, rows_per_cta;
-  float eps;
+  int tokens, n, d, rope_dims;
+  int tpc, rows_per_cta;                // tokens of a CTA; rows of its token (tpc = 1) that it takes
+  float eps, inv_d;
   TreePlan plan;
   double theta[kNrMaxPairs];
 };
@@ -99,33 +105,82 @@ template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4&
   }
 }
 
-template <typename T, int LPR, int NCH, bool kTree>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
-  constexpr int VEC = Vec16<T>::N;
+// Pairs of fp32 in one 64-bit register.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2_unpack(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename T> __device__ __forceinline__ void f2_load(const uint4& raw, uint64_t* o);
+template <> __device__ __forceinline__ void f2_load<float>(const uint4& raw, uint64_t* o) {
+  o[0] = f2_pack(__uint_as_float(raw.x), __uint_as_float(raw.y));
+  o[1] = f2_pack(__uint_as_float(raw.z), __uint_as_float(raw.w));
+}
+template <> __device__ __forceinline__ void f2_load<__nv_bfloat16>(const uint4& raw, uint64_t* o) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <typename T> __device__ __forceinline__ uint4 f2_store(const uint64_t* v);
+template <> __device__ __forceinline__ uint4 f2_store<float>(const uint64_t* v) {
+  const float2 a = f2_unpack(v[0]), b = f2_unpack(v[1]);
+  return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+}
+template <> __device__ __forceinline__ uint4 f2_store<__nv_bfloat16>(const uint64_t* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = f2_unpack(v[i]);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// kFull: every lane's NCH pieces exist (d = LPR * NCH * VEC).
+template <typename T, int LPR, int NCH, bool kFull, bool kTree>
+__global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr int VEC = Vec16<T>::N, V2 = VEC / 2;
   constexpr int RPW = 32 / LPR;                       // rows a warp takes at once
   constexpr int RPC = RPW * (kNrThreads / 32);        // rows the CTA takes at once
-  constexpr int U = NCH >= 4 ? 2 : 4;                 // rows of a lane in flight
-  __shared__ float2 cs_s[kNrMaxPairs];
+  constexpr int U = NCH >= 2 ? 2 : 4;                 // rows of a lane in flight
+  __shared__ float2 cs_s[kNrTable];
+  __shared__ int pos_s[kNrMaxTokens];
+  __shared__ int64_t off_s[4][kNrMaxTokens];          // token's offset in q, k, q_out, k_out
   __shared__ int par_s[kTree ? kTreeMaxNodes : 1], path_s[kTree ? kTreeMaxNodes : 1], t_s;
   griddep_wait();
   griddep_launch_dependents();
-  const int tok = blockIdx.x, b = tok / p.n, i = tok - b * p.n;
+  const int tok0 = blockIdx.x * p.tpc;
   const int lane = threadIdx.x & 31, sub = lane % LPR;
   const int slot = (threadIdx.x >> 5) * RPW + lane / LPR;
-  const int rows = p.heads[0] + p.heads[1];
-  const int r_begin = blockIdx.y * p.rows_per_cta, r_end = min(rows, r_begin + p.rows_per_cta);
-  const int nch = p.d / VEC;
+  const int heads = p.heads[0] + p.heads[1];
+  const int npair = p.rope_dims >> 1;
 
-  int t = 0;
   if constexpr (kTree) {
-    t = tree_node(p.plan.parents, p.plan.pos, b, p.n, i, par_s, path_s, &t_s);
+    const int b = tok0 / p.n, i = tok0 - b * p.n;
+    const int t = tree_node(p.plan.parents, p.plan.pos, b, p.n, i, par_s, path_s, &t_s);
     if (blockIdx.y == 0) {
       const TreePlan& L = p.plan;
       if (threadIdx.x == 0) {
-        L.node_pos[tok] = t;
-        L.sel_pos[tok] = t < 0 ? -1 : L.pos[b] - 1;
+        L.node_pos[tok0] = t;
+        L.sel_pos[tok0] = t < 0 ? -1 : L.pos[b] - 1;
       }
-      int* list = L.list + (int64_t)tok * (L.w + L.T);
+      int* list = L.list + (int64_t)tok0 * (L.w + L.T);
       int count = 0;
       if (t >= 0) {
         const int p0 = L.pos[b], lo = max(0, t - L.w + 1);
@@ -142,87 +197,118 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
               list[count++] = (ROW_DRAFT << kRowShift) | (b * L.T + path_s[q - p0]);
         }
       }
-      if (threadIdx.x == 0) L.info[tok] = make_int4(t, t < 0 ? 0 : min(L.N, L.pos[b] / L.m), count, 0);
+      if (threadIdx.x == 0) L.info[tok0] = make_int4(t, t < 0 ? 0 : min(L.N, L.pos[b] / L.m), count, 0);
     }
+    if (t < 0) return;
+    if (threadIdx.x == 0) pos_s[0] = t;
   } else {
-    t = p.pos[tok];
+    if (threadIdx.x < p.tpc) pos_s[threadIdx.x] = tok0 + threadIdx.x < p.tokens ? p.pos[tok0 + threadIdx.x] : -1;
   }
-  if (t < 0) return;
+  if (threadIdx.x < 4 * p.tpc) {
+    const int w = threadIdx.x & 3, q = threadIdx.x >> 2, tok = tok0 + q, b = tok / p.n, i = tok - b * p.n;
+    const int64_t* st = w < 2 ? p.xs[w] : p.ys[w - 2];
+    off_s[w][q] = b * st[0] + i * st[1];
+  }
+  __syncthreads();
 
+  // rows of this CTA: [row_begin, row_end) of one token, or all of tpc tokens
+  const int row_begin = blockIdx.y * p.rows_per_cta;
+  const int row_end = p.tpc > 1 ? heads : min(heads, row_begin + p.rows_per_cta);
+  const int n_rows = p.tpc > 1 ? p.tpc * heads : row_end - row_begin;
+  const int nch = p.d / VEC;
+  int tk = 0, row = row_begin + slot;                 // this lane group's next row
+  if (p.tpc > 1) { tk = slot / heads; row = slot - tk * heads; }
+  const int step_t = p.tpc > 1 ? RPC / heads : 0, step_r = RPC - step_t * heads;
   bool have_cs = false;
   int which = -1;
-  float gain[NCH][VEC];
-  for (int r0 = r_begin; r0 < r_end; r0 += U * RPC) {
+  uint64_t gain[NCH][V2];
+  for (int r0 = 0; r0 < n_rows; r0 += U * RPC) {
     uint4 raw[U][NCH];
+    T* out[U];
+    int ut[U];                                        // token of the row (-1: nothing to do)
+    bool uk[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = r0 + u * RPC + slot;
+      const bool in = r0 + u * RPC + slot < n_rows && pos_s[tk] >= 0;
       const int k = row >= p.heads[0];
-      const T* x = static_cast<const T*>(p.x[k]) + b * p.xs[k][0] + i * p.xs[k][1] +
-                   (row - k * p.heads[0]) * p.xs[k][2];
+      ut[u] = in ? tk : -1;
+      uk[u] = k;
+      if (in) {
+        const int h = row - k * p.heads[0];
+        const T* x = static_cast<const T*>(p.x[k]) + (off_s[k][tk] + h * p.xs[k][2] + sub * VEC);
+        out[u] = static_cast<T*>(p.y[k]) + (off_s[2 + k][tk] + h * p.d + sub * VEC);
 #pragma unroll
-      for (int q = 0; q < NCH; ++q) {
-        const int ch = sub + LPR * q;
-        if (row < r_end && ch < nch) raw[u][q] = __ldg(reinterpret_cast<const uint4*>(x + ch * VEC));
+        for (int q = 0; q < NCH; ++q) {
+          if (kFull || sub + LPR * q < nch) raw[u][q] = __ldg(reinterpret_cast<const uint4*>(x + LPR * q * VEC));
+        }
       }
+      row += step_r;
+      tk += step_t;
+      if (p.tpc > 1 && row >= heads) { row -= heads; ++tk; }
     }
     if (!have_cs) {
       // (uniform over the CTA: the first turn of every warp)
-      for (int j = threadIdx.x; j < p.rope_dims / 2; j += blockDim.x)
-        rope_sincos((double)t, p.theta[j], &cs_s[j].x, &cs_s[j].y);
+      for (int j = threadIdx.x; j < p.tpc * npair; j += blockDim.x) {
+        const int q = j / npair;
+        float2 c;
+        rope_sincos((double)pos_s[q], p.theta[j - q * npair], &c.x, &c.y);
+        cs_s[j] = c;
+      }
       __syncthreads();
       have_cs = true;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = r0 + u * RPC + slot;
-      if (r0 + u * RPC >= r_end) break;               // (uniform over the CTA)
-      const int k = row >= p.heads[0];
+      if (r0 + u * RPC >= n_rows) break;              // (uniform over the CTA)
+      const int k = uk[u];
       if (k != which) {
         which = k;
 #pragma unroll
         for (int q = 0; q < NCH; ++q) {
           const int ch = sub + LPR * q;
 #pragma unroll
-          for (int e = 0; e < VEC; e += 4) {
+          for (int e = 0; e < V2; e += 2) {
             float4 g = make_float4(1.f, 1.f, 1.f, 1.f);
             if (p.norm[k] && p.gain[k] && ch < nch)
-              g = __ldg(reinterpret_cast<const float4*>(p.gain[k] + ch * VEC + e));
-            gain[q][e] = g.x; gain[q][e + 1] = g.y; gain[q][e + 2] = g.z; gain[q][e + 3] = g.w;
+              g = __ldg(reinterpret_cast<const float4*>(p.gain[k] + ch * VEC + 2 * e));
+            gain[q][e] = f2_pack(g.x, g.y);
+            gain[q][e + 1] = f2_pack(g.z, g.w);
           }
         }
       }
-      float v[NCH][VEC];
-      float ss = 0.f;
+      const bool in = ut[u] >= 0;
+      uint64_t v[NCH][V2], s2 = 0;
 #pragma unroll
       for (int q = 0; q < NCH; ++q) {
-        if (row < r_end && sub + LPR * q < nch) {
-          unpack16<T>(raw[u][q], v[q]);
+        if (in && (kFull || sub + LPR * q < nch)) {
+          f2_load<T>(raw[u][q], v[q]);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) ss = fmaf(v[q][e], v[q][e], ss);
+          for (int e = 0; e < V2; ++e) s2 = f2_fma(v[q][e], v[q][e], s2);
         }
       }
+      const float2 s1 = f2_unpack(s2);
+      float ss = s1.x + s1.y;
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float inv = p.norm[k] ? rsqrtf(ss / (float)p.d + p.eps) : 1.f;
-      T* y = static_cast<T*>(p.y[k]) + b * p.ys[k][0] + i * p.ys[k][1] + (row - k * p.heads[0]) * p.ys[k][2];
+      const float inv = p.norm[k] ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f;
+      const uint64_t inv2 = f2_pack(inv, inv);
 #pragma unroll
       for (int q = 0; q < NCH; ++q) {
         const int ch = sub + LPR * q;
-        if (row < r_end && ch < nch) {
+        if (in && (kFull || ch < nch)) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[q][e] *= inv * gain[q][e];
-          const int j0 = ch * VEC - (p.d - p.rope_dims);
+          for (int e = 0; e < V2; ++e) v[q][e] = f2_mul(v[q][e], f2_mul(gain[q][e], inv2));
+          const int j0 = (ch * VEC - (p.d - p.rope_dims)) >> 1;
+          if (j0 + V2 > 0) {
 #pragma unroll
-          for (int e = 0; e < VEC; e += 2) {
-            if (j0 + e >= 0) {
-              const float2 c = cs_s[(j0 + e) >> 1];
-              const float x0 = v[q][e], x1 = v[q][e + 1];
-              v[q][e] = x0 * c.x - x1 * c.y;
-              v[q][e + 1] = x0 * c.y + x1 * c.x;
+            for (int e = 0; e < V2; ++e) {
+              if (j0 + e >= 0) {
+                const float2 c = cs_s[ut[u] * npair + j0 + e], x = f2_unpack(v[q][e]);
+                v[q][e] = f2_pack(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+              }
             }
           }
-          store16(y + ch * VEC, v[q]);
+          *reinterpret_cast<uint4*>(out[u] + LPR * q * VEC) = f2_store<T>(v[q]);
         }
       }
     }
