@@ -292,16 +292,24 @@ def cp_attn_merge(partials, sinks, pos, *, H, d, rope_dims, dtype=torch.bfloat16
     return out
 
 
-def _on(stream, dev):
-    """Context in which a call's tensors are allocated and its kernels launched:
-    the given stream, or the current stream of the tensors' device."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(stream, dev, call, *args):
+    """call(*args) with the tensors' device current and the given stream (or
+    the device's current one) as the stream of its allocations and kernels."""
     if dev.type != "cuda":
         raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return torch.cuda.device(dev)
+        with torch.cuda.stream(stream):
+            return call(*args)
+    if torch.cuda.current_device() == dev.index:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
 
 
 def _arg(name, t, dev, shape, dtype, optional=False):
@@ -310,20 +318,20 @@ def _arg(name, t, dev, shape, dtype, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _ints(name, t, dev, shape, keep):
     """Pointer of an int32 argument (other integer tensors are converted)."""
-    if t.dtype != torch.int32 or not t.is_contiguous():
+    if t.dtype is not torch.int32 or not t.is_contiguous():
         if t.dtype.is_floating_point or t.device != dev:
             raise TypeError(f"{name} must be an integer tensor on {dev}")
         t = t.to(torch.int32).contiguous()
@@ -333,10 +341,46 @@ def _ints(name, t, dev, shape, keep):
 
 def _floats(name, t, dev, shape, keep, optional=True):
     """Pointer of an fp32 argument (other floating tensors are converted)."""
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous()):
+    if t is not None and (t.dtype is not torch.float32 or not t.is_contiguous()):
         t = t.contiguous().float()
         keep.append(t)
     return _arg(name, t, dev, shape, torch.float32, optional)
+
+
+def _heads(name, t, out, gain, dev, dt, B, n, d, keep):
+    """One side of qk_norm_rope: (heads, strides or None, pointers of rows, output and gain, output)."""
+    shape = t.shape
+    if t.dtype is not dt or t.device != dev or len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != d:
+        raise ValueError(f"{name}: {tuple(shape)} {t.dtype} on {t.device} does not match the other rows")
+    strides = None
+    if not t.is_contiguous():
+        strides = t.stride()
+        if d > 1 and strides[3] != 1:
+            raise ValueError(f"{name}: the dims of a head must be contiguous")
+    if out is None:
+        out = torch.empty_like(t, memory_format=torch.contiguous_format)
+        o = out.data_ptr()
+    else:
+        o = _arg(name + "_out", out, dev, shape, dt)
+    return shape[2], strides, t.data_ptr(), o, _floats(name + "_gain", gain, dev, (d,), keep), out
+
+
+def _norm_rope(q, k, pos, rope_dims, q_gain, k_gain, q_norm, k_norm, rope_base, eps, q_out, k_out):
+    x = q if q is not None else k
+    dev, dt, keep = x.device, x.dtype, []
+    B, n, _, d = x.shape
+    a = N.NormRopeArgs(dtype=_dt(x), B=B, n=n, d=d, rope_dims=rope_dims, rope_base=rope_base, eps=eps, q_norm=bool(q_norm),
+                       k_norm=bool(k_norm), pos=_ints("pos", pos, dev, (B, n), keep))
+    if q is not None:
+        a.HQ, st, a.q, a.q_out, a.q_gain, q_out = _heads("q", q, q_out, q_gain, dev, dt, B, n, d, keep)
+        if st is not None:
+            a.q_stride[:] = st[:3]
+    if k is not None:
+        a.HK, st, a.k, a.k_out, a.k_gain, k_out = _heads("k", k, k_out, k_gain, dev, dt, B, n, d, keep)
+        if st is not None:
+            a.k_stride[:] = st[:3]
+    N.check(N.lib().qk_norm_rope(C.byref(a), _raw_stream(dev.index)), "qk_norm_rope")
+    return (q_out if q is not None else None, k_out if k is not None else None)
 
 
 def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True, k_norm=True, rope_base=10000.0,
@@ -352,32 +396,35 @@ def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True,
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is required")
+    _dt(x)
+    return _on(stream, x.device, _norm_rope, q, k, pos, rope_dims, q_gain, k_gain, q_norm, k_norm, rope_base, eps, q_out,
+               k_out)
+
+
+def _tree_compress(kind, streams, ring, pos, parents, bias_a, m, bias_b, gain, rms_norm, rope_dims, rope_base, eps, out,
+                   out_scale):
+    csa = kind == "csa"
+    x = streams[0]
     dev, dt, keep = x.device, x.dtype, []
     code = _dt(x)
-    B, n, _, d = x.shape
-    with _on(stream, dev):
-        a = N.NormRopeArgs(dtype=code, B=B, n=n, d=d, rope_dims=rope_dims, rope_base=rope_base, eps=eps,
-                           q_norm=int(bool(q_norm)), k_norm=int(bool(k_norm)), pos=_ints("pos", pos, dev, (B, n), keep))
-        outs = []
-        for name, t, o, gain in (("q", q, q_out, q_gain), ("k", k, k_out, k_gain)):
-            if t is None:
-                outs.append(None)
-                continue
-            if t.device != dev or t.dtype != dt or t.dim() != 4 or (t.shape[0], t.shape[1], t.shape[3]) != (B, n, d):
-                raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device} does not match the other rows")
-            if d > 1 and t.stride(3) != 1:
-                raise ValueError(f"{name}: the dims of a head must be contiguous")
-            if o is None:
-                o = torch.empty(t.shape, dtype=dt, device=dev)
-            setattr(a, "H" + name.upper(), t.shape[2])
-            if not t.is_contiguous():
-                setattr(a, name + "_stride", (N.i64 * 3)(*t.stride()[:3]))
-            setattr(a, name, t.data_ptr())
-            setattr(a, name + "_out", _arg(name + "_out", o, dev, t.shape, dt))
-            setattr(a, name + "_gain", _floats(name + "_gain", gain, dev, (d,), keep))
-            outs.append(o)
-        N.check(N.lib().qk_norm_rope(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "qk_norm_rope")
-    return tuple(outs)
+    B, T, c = shape = x.shape
+    f8 = out_scale is not None
+    odt = torch.uint8 if f8 else dt
+    if out is None:
+        out = torch.zeros(B, T, c, dtype=odt, device=dev)
+    p = [_arg("streams", t, dev, shape, dt) for t in streams]
+    a = N.TreeCompressArgs(
+        kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
+        rms_norm=bool(rms_norm), rope_dims=rope_dims, rope_base=rope_base, eps=eps,
+        pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
+        a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
+        ring=_arg("ring", ring, dev, (B, 2 * m, 4, c) if csa else (B, m, 2, c), dt),
+        bias_a=_floats("bias_a", bias_a, dev, (m, c), keep, False),
+        bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
+        out=_arg("out", out, dev, shape, odt),
+        out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
+    N.check(N.lib().tree_compress(C.byref(a), _raw_stream(dev.index)), "tree_compress")
+    return out
 
 
 def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, gain=None, rms_norm=True, rope_dims=0,
@@ -391,31 +438,10 @@ def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, 
     out [B, T, c]: row i is written iff node i's token ends a block, the others
     are left as they were (a new out starts at zero).  With out_scale
     [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys."""
-    csa = kind == "csa"
-    if len(streams) != (4 if csa else 2):
+    if len(streams) != (4 if kind == "csa" else 2):
         raise ValueError("csa takes four streams (a, b, za, zb), hca two (a, za)")
-    x = streams[0]
-    dev, dt, keep = x.device, x.dtype, []
-    code = _dt(x)
-    B, T, c = x.shape
-    R, S = (2 * m, 4) if csa else (m, 2)
-    with _on(stream, dev):
-        f8 = out_scale is not None
-        odt = torch.uint8 if f8 else dt
-        if out is None:
-            out = torch.zeros(B, T, c, dtype=odt, device=dev)
-        p = [_arg(f"streams[{i}]", t, dev, (B, T, c), dt) for i, t in enumerate(streams)]
-        a = N.TreeCompressArgs(
-            kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
-            rms_norm=int(bool(rms_norm)), rope_dims=rope_dims, rope_base=rope_base, eps=eps,
-            pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
-            a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
-            ring=_arg("ring", ring, dev, (B, R, S, c), dt), bias_a=_floats("bias_a", bias_a, dev, (m, c), keep, False),
-            bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
-            out=_arg("out", out, dev, (B, T, c), odt),
-            out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
-        N.check(N.lib().tree_compress(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "tree_compress")
-    return out
+    return _on(stream, streams[0].device, _tree_compress, kind, streams, ring, pos, parents, bias_a, m, bias_b, gain,
+               rms_norm, rope_dims, rope_base, eps, out, out_scale)
 
 
 def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, rope_dims, draft=None, k=0, qI=None,
@@ -433,8 +459,8 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     if out is None:
         out = torch.zeros(q.shape, dtype=dt, device=dev)
     a = N.TreeAttnArgs(kind=N.CSA if csa else N.HCA, dtype=code, B=B, T=T, H=H, d=d, N_cap=Nc, m=m, w=w,
-                       rope_dims=rope_dims, rope_base=rope_base, eps=eps, scale=scale, q_norm=int(bool(q_norm)),
-                       kv_norm=int(bool(kv_norm)), q=_arg("q", q, dev, q.shape, dt),
+                       rope_dims=rope_dims, rope_base=rope_base, eps=eps, scale=scale, q_norm=bool(q_norm),
+                       kv_norm=bool(kv_norm), q=_arg("q", q, dev, q.shape, dt),
                        pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
                        q_gain=_floats("q_gain", q_gain, dev, (d,), keep),
                        kv_gain=_floats("kv_gain", kv_gain, dev, (d,), keep),
@@ -464,6 +490,20 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     return a, out, keep
 
 
+def _attn_tree(args, kw, workspace):
+    a, out, keep = tree_attn_args(*args, **kw)
+    dev = out.device
+    L = N.lib()
+    nbytes = L.csahca_tree_workspace_size(C.byref(a))
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    a.workspace = _arg("workspace", workspace, dev, workspace.shape, workspace.dtype)
+    a.workspace_bytes = workspace.numel() * workspace.element_size()
+    N.check(L.compressed_attn_tree(C.byref(a), _raw_stream(dev.index)), "compressed_attn_tree")
+    del keep
+    return out
+
+
 def compressed_attn_tree(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, rope_dims, workspace=None,
                          stream=None, **kw):
     """Attention of every node of draft trees over one CSA or HCA layer's caches:
@@ -477,18 +517,8 @@ def compressed_attn_tree(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *,
     (kI_scale) and draft_kI (draft_kI_scale) for the lightning indexer; idx_out
     [B, T, k] receives the selection.  Rows of places without a node are left as
     they were (a new out starts at zero).  Returns out [B, T, H, d]."""
-    dev = q.device
-    with _on(stream, dev):
-        a, out, keep = tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, m=m, rope_dims=rope_dims, **kw)
-        L = N.lib()
-        nbytes = L.csahca_tree_workspace_size(C.byref(a))
-        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        a.workspace = _arg("workspace", workspace, dev, workspace.shape, workspace.dtype)
-        a.workspace_bytes = workspace.numel() * workspace.element_size()
-        N.check(L.compressed_attn_tree(C.byref(a), torch.cuda.current_stream(dev).cuda_stream), "compressed_attn_tree")
-    del keep
-    return out
+    return _on(stream, q.device, _attn_tree, (kind, q, pos, parents, kv_cache, win, kv_raw, sinks),
+               dict(kw, m=m, rope_dims=rope_dims), workspace)
 
 
 def device_error(stream=None) -> int:

@@ -1269,8 +1269,17 @@ int run_cp_attn_merge(const csahca_cp_merge_args* a, void* stream) {
 // ------------------------------------------------------------ qk_norm_rope --
 
 // theta of the first r / 2 pairs, in double, into a kernel parameter array.
+// (the last r and base of the calling thread are remembered: 32 powers are a
+// microsecond of a call that may be four)
 void rope_theta_pairs(double* theta, int r, double base) {
-  for (int j = 0; j < r / 2; ++j) theta[j] = pow(base, -2.0 * j / r);
+  static thread_local int last_r = -1;
+  static thread_local double last_base = 0.0, table[kNrMaxPairs];
+  if (r != last_r || base != last_base) {
+    for (int j = 0; j < r / 2; ++j) table[j] = pow(base, -2.0 * j / r);
+    last_r = r;
+    last_base = base;
+  }
+  memcpy(theta, table, sizeof(double) * (size_t)(r / 2));
 }
 
 template <typename T, int LPR, int NCH, bool kTree>
@@ -1557,7 +1566,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   p.sinks = a->sinks; p.list_stride = a->w + a->T; p.k = a->k; p.N = a->N_cap; p.T = a->T;
   p.splits = L.splits; p.n_items = nodes * L.splits; p.scale_log2 = scale * kLog2e; p.rope_dims = a->rope_dims;
   p.out = static_cast<__nv_bfloat16*>(a->out); p.partial = ws + L.partial;
-  rope_theta_table(p.theta, a->rope_dims, base);
+  rope_theta_pairs(p.theta, a->rope_dims, base);              // (the rest stays zero)
   // rows of 512 bf16 as [chunk 8][row][64]: a key box is four chunks of 64
   // rows (32 KB), the query box all 8 chunks of a node's 64 heads
   CUtensorMap m_rows, m_q;
