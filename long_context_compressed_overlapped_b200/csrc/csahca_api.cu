@@ -1378,10 +1378,11 @@ int run_norm_rope(const csahca_norm_rope_args* a, void* stream) {
 
 template <typename T, bool kCSA>
 void launch_tree_compress(const TreeCompressParams& p, int nodes, cudaStream_t s) {
-  constexpr int smem = tree_compress_smem<T>();
+  constexpr int smem = tree_compress_smem<T, kCSA>();
   cudaFuncSetAttribute(tree_compress_kernel<T, kCSA>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   CSAHCA_TRACE("tree_compress", s);
-  launch_k(tree_compress_kernel<T, kCSA>, dim3((unsigned)nodes), dim3(kTcpThreads), smem, s, p);
+  launch_k(tree_compress_kernel<T, kCSA>, dim3((unsigned)nodes), dim3(tree_compress_threads<kCSA>()),
+           smem, s, p);
 }
 
 int run_tree_compress(const csahca_tree_compress_args* a, void* stream) {

@@ -60,35 +60,38 @@ struct NormRopeParams {
   double theta[kNrMaxPairs];
 };
 
-// The path of node i: path[0] the first drafted token .. path[depth] = i.
-// Returns the depth, or -1 if i or one of its ancestors is no node.  A parent
-// that is not below its child ends the walk as no node (error word 2), so the
-// walk always ends.
-__device__ __forceinline__ int tree_path(const int* parents, int i, int* path) {
-  int up = 0;
-  for (int j = i; j >= 0;) {
-    const int p = parents[j];
-    if (p < -1) return -1;
-    if (p >= j) { raise_device_error(DEVERR_BAD_INDEX); return -1; }
-    path[up++] = j;
-    j = p;
-  }
-  for (int a = 0, b = up - 1; a < b; ++a, --b) { const int s = path[a]; path[a] = path[b]; path[b] = s; }
-  return up - 1;
-}
+// A node of a draft tree, as the threads of its CTA see it: its sequence's
+// first position, its own (-1: no node), and up[k], its k-th ancestor (up[0] the
+// node itself, up[t - pos0] a first drafted token).
+struct TreeNode {
+  int par[kTreeMaxNodes], up[kTreeMaxNodes];
+  int pos0, t;
+  __device__ __forceinline__ int at(int position) const { return up[t - position]; }   // path node at a position >= pos0
+};
 
-// Position of the token, or -1 for none; every thread of the CTA calls it.
-__device__ __forceinline__ int tree_node(const int* parents, const int* pos, int b, int T, int i, int* par_s,
-                                         int* path_s, int* t_s) {
-  for (int j = threadIdx.x; j <= i; j += blockDim.x) par_s[j] = parents[(int64_t)b * T + j];
+// Fills it; every thread of the CTA calls it, and gets the node's position.  A
+// parent that is not below its child ends the walk as no node (error word 2),
+// so the walk always ends.
+__device__ __forceinline__ int tree_node(const int* parents, const int* pos, int b, int T, int i, TreeNode* nd) {
+  const int p0 = threadIdx.x == 0 ? pos[b] : 0;
+  for (int j = threadIdx.x; j <= i; j += blockDim.x) nd->par[j] = parents[(int64_t)b * T + j];
   __syncthreads();
   if (threadIdx.x == 0) {
-    const int p0 = pos[b];
-    const int depth = p0 < 0 ? -1 : tree_path(par_s, i, path_s);
-    *t_s = depth < 0 || p0 > INT32_MAX - kTreeMaxNodes ? -1 : p0 + depth;
+    int depth = -1;
+    if (p0 >= 0 && p0 <= INT32_MAX - kTreeMaxNodes) {
+      for (int j = i; j >= 0;) {
+        const int p = nd->par[j];
+        if (p < -1) { depth = -1; break; }
+        if (p >= j) { raise_device_error(DEVERR_BAD_INDEX); depth = -1; break; }
+        nd->up[++depth] = j;
+        j = p;
+      }
+    }
+    nd->pos0 = p0;
+    nd->t = depth < 0 ? -1 : p0 + depth;
   }
   __syncthreads();
-  return *t_s;
+  return nd->t;
 }
 
 template <typename T> __device__ __forceinline__ void unpack16(const uint4& raw, float* o);
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
   __shared__ float2 cs_s[kNrTable];
   __shared__ int pos_s[kNrMaxTokens];
   __shared__ int64_t off_s[4][kNrMaxTokens];          // token's offset in q, k, q_out, k_out
-  __shared__ int par_s[kTree ? kTreeMaxNodes : 1], path_s[kTree ? kTreeMaxNodes : 1], t_s;
+  __shared__ TreeNode node_s;                         // (kTree)
   griddep_wait();
   griddep_launch_dependents();
   const int tok0 = blockIdx.x * p.tpc;
@@ -173,31 +176,32 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
 
   if constexpr (kTree) {
     const int b = tok0 / p.n, i = tok0 - b * p.n;
-    const int t = tree_node(p.plan.parents, p.plan.pos, b, p.n, i, par_s, path_s, &t_s);
+    const int t = tree_node(p.plan.parents, p.plan.pos, b, p.n, i, &node_s);
+    const int p0 = node_s.pos0;
     if (blockIdx.y == 0) {
       const TreePlan& L = p.plan;
       if (threadIdx.x == 0) {
         L.node_pos[tok0] = t;
-        L.sel_pos[tok0] = t < 0 ? -1 : L.pos[b] - 1;
+        L.sel_pos[tok0] = t < 0 ? -1 : p0 - 1;
       }
       int* list = L.list + (int64_t)tok0 * (L.w + L.T);
       int count = 0;
       if (t >= 0) {
-        const int p0 = L.pos[b], lo = max(0, t - L.w + 1);
+        const int lo = max(0, t - L.w + 1);
         const int nwin = L.w > 0 ? t - lo + 1 : 0;
         for (int j = threadIdx.x; j < nwin; j += blockDim.x) {
           const int q = lo + j;
           list[j] = q < p0 ? (ROW_RING << kRowShift) | (b * L.w + q % L.w)
-                           : (ROW_TREE << kRowShift) | (b * L.T + path_s[q - p0]);
+                           : (ROW_TREE << kRowShift) | (b * L.T + node_s.at(q));
         }
         count = nwin;
         if (L.list_drafts && threadIdx.x == 0) {
           for (int q = p0; q <= t; ++q)
             if ((q + 1) % L.m == 0 && (q + 1) / L.m - 1 < L.N)
-              list[count++] = (ROW_DRAFT << kRowShift) | (b * L.T + path_s[q - p0]);
+              list[count++] = (ROW_DRAFT << kRowShift) | (b * L.T + node_s.at(q));
         }
       }
-      if (threadIdx.x == 0) L.info[tok0] = make_int4(t, t < 0 ? 0 : min(L.N, L.pos[b] / L.m), count, 0);
+      if (threadIdx.x == 0) L.info[tok0] = make_int4(t, t < 0 ? 0 : min(L.N, p0 / L.m), count, 0);
     }
     if (t < 0) return;
     if (threadIdx.x == 0) pos_s[0] = t;

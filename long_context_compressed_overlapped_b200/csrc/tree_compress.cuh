@@ -11,20 +11,25 @@
 //
 // One CTA = one node; a node that completes nothing leaves at once.  A thread
 // owns a 16-byte vector of channels and every G-th token of the pool, so that
-// all rows of the pool are asked for in one or few round trips to L2 (the call
-// is bound by them, not by its few hundred KB); the G partial softmaxes
-// (max, sum, weighted sum) are joined in shared memory.
+// all rows of the pool are asked for in one or few round trips to L2: the call
+// is bound by those and by the walk up the tree, not by its few hundred KB.
+// The G partial softmaxes (max, sum, weighted sum) are joined in shared
+// memory, a channel a thread.  256 threads for the 2m rows of CSA (three CTAs an
+// SM; 512 at one an SM ran in four waves, 22 us instead of 9 for 512 nodes),
+// 512 for the m' of HCA.
 #pragma once
-#include "compress.cuh"
 #include "norm_rope.cuh"
+#include "tc_common.cuh"
 
 namespace csahca {
 
-constexpr int kTcpThreads = 512;
 constexpr int kTcpMaxTokens = 512;      // 2m (CSA), m (HCA)
-constexpr int kTcpBatch = 4;            // tokens of a thread in flight
+constexpr float kLog2eF = 1.4426950408889634f;
 
-template <typename T> constexpr int tree_compress_smem() { return 3 * Vec16<T>::N * kTcpThreads * 4; }
+template <bool kCSA> __host__ __device__ constexpr int tree_compress_threads() { return kCSA ? 256 : 512; }
+template <typename T, bool kCSA> constexpr int tree_compress_smem() {
+  return 3 * Vec16<T>::N * tree_compress_threads<kCSA>() * 4;
+}
 
 struct TreeCompressParams {
   const int* parents; const int* pos;
@@ -38,35 +43,37 @@ struct TreeCompressParams {
 };
 
 template <typename T, bool kCSA>
-__global__ void __launch_bounds__(kTcpThreads) tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
-  constexpr int VEC = Vec16<T>::N;
+__global__ void __launch_bounds__(tree_compress_threads<kCSA>(), kCSA ? 3 : 1)
+tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
+  constexpr int VEC = Vec16<T>::N, kThreads = tree_compress_threads<kCSA>();
   constexpr int S = kCSA ? 4 : 2;
+  constexpr int kTcpBatch = kCSA ? 2 : 4;             // tokens of a thread in flight
   // partial softmaxes by vector element: thread x's element e at [e][x], conflict-free
   extern __shared__ __align__(16) float tcp_smem[];
-  float (*st_mx)[kTcpThreads] = reinterpret_cast<float (*)[kTcpThreads]>(tcp_smem);
-  float (*st_s)[kTcpThreads] = st_mx + VEC;
-  float (*st_acc)[kTcpThreads] = st_s + VEC;
+  float (*st_mx)[kThreads] = reinterpret_cast<float (*)[kThreads]>(tcp_smem);
+  float (*st_s)[kThreads] = st_mx + VEC;
+  float (*st_acc)[kThreads] = st_s + VEC;
   __shared__ int src_s[kTcpMaxTokens];  // >= 0: node of the tree; < 0: ring slot -1 - src
-  __shared__ int par_s[kTreeMaxNodes], path_s[kTreeMaxNodes], t_s;
-  __shared__ float red_s[kTcpThreads / 32];
+  __shared__ TreeNode node_s;
+  __shared__ float red_s[kThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int tok = blockIdx.x, b = tok / p.T, i = tok - b * p.T;
-  const int t = tree_node(p.parents, p.pos, b, p.T, i, par_s, path_s, &t_s);
+  const int t = tree_node(p.parents, p.pos, b, p.T, i, &node_s);
   const int m = p.m, c = p.c;
   if (t < 0 || (t + 1) % m != 0) return;
   const int tid = threadIdx.x, lane = tid & 31;
   const int R = kCSA ? 2 * m : m;
-  const int p0 = p.pos[b];
+  const int p0 = node_s.pos0;
   const int blk = (t + 1) / m - 1;
   const int J0 = (kCSA && blk == 0) ? m : 0;          // entry 0 has no preceding block
-  for (int j = J0 + tid; j < R; j += kTcpThreads) {
+  for (int j = J0 + tid; j < R; j += kThreads) {
     const int q = t + 1 - R + j;                      // token j of the pool (CSA: preceding block first)
-    src_s[j] = q >= p0 ? path_s[q - p0] : -1 - q % R;
+    src_s[j] = q >= p0 ? node_s.at(q) : -1 - q % R;
   }
   __syncthreads();
 
-  const int nv = c / VEC, G = kTcpThreads / nv;       // nv <= 128: G >= 4
+  const int nv = c / VEC, G = kThreads / nv;          // nv <= 128: G >= 2
   const int vec = tid % nv, grp = tid / nv, ch0 = vec * VEC;
   float mx[VEC], s[VEC], acc[VEC];
 #pragma unroll
@@ -74,6 +81,7 @@ __global__ void __launch_bounds__(kTcpThreads) tree_compress_kernel(const __grid
   if (grp < G) {
     for (int jb = J0 + grp; jb < R; jb += G * kTcpBatch) {
       uint4 rv[kTcpBatch], rz[kTcpBatch];
+      float4 rb[kTcpBatch][VEC / 4];
 #pragma unroll
       for (int u = 0; u < kTcpBatch; ++u) {
         const int j = jb + u * G;
@@ -92,64 +100,90 @@ __global__ void __launch_bounds__(kTcpThreads) tree_compress_kernel(const __grid
           }
           rv[u] = __ldg(reinterpret_cast<const uint4*>(rv_p));
           rz[u] = __ldg(reinterpret_cast<const uint4*>(rz_p));
+          const float* bias = kCSA ? (j < m ? p.bias_b + (int64_t)j * c : p.bias_a + (int64_t)(j - m) * c)
+                                   : p.bias_a + (int64_t)j * c;
+#pragma unroll
+          for (int e = 0; e < VEC / 4; ++e) rb[u][e] = __ldg(reinterpret_cast<const float4*>(bias + ch0) + e);
+        }
+      }
+      // the batch's logits in log2 units (-inf: weight 0, and where there is no
+      // token), one new maximum and one rescale of the running sums a channel
+      float z[kTcpBatch][VEC];
+#pragma unroll
+      for (int u = 0; u < kTcpBatch; ++u) {
+        if (jb + u * G < R) {
+          unpack16<T>(rz[u], z[u]);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            z[u][e] = (z[u][e] + reinterpret_cast<const float*>(&rb[u][e / 4])[e % 4]) * kLog2eF;
+        } else {
+          rv[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) z[u][e] = -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float M = mx[e];
+#pragma unroll
+        for (int u = 0; u < kTcpBatch; ++u) M = fmaxf(M, z[u][e]);
+        const float Ms = M == -INFINITY ? 0.f : M, f = fast_exp2(mx[e] - Ms);
+        mx[e] = M;
+        s[e] *= f;
+        acc[e] *= f;
+#pragma unroll
+        for (int u = 0; u < kTcpBatch; ++u) {
+          z[u][e] = fast_exp2(z[u][e] - Ms);
+          s[e] += z[u][e];
         }
       }
 #pragma unroll
       for (int u = 0; u < kTcpBatch; ++u) {
-        const int j = jb + u * G;
-        if (j < R) {
-          float v[VEC], z[VEC];
-          unpack16<T>(rv[u], v);
-          unpack16<T>(rz[u], z);
-          const float* bias = kCSA ? (j < m ? p.bias_b + (int64_t)j * c : p.bias_a + (int64_t)(j - m) * c)
-                                   : p.bias_a + (int64_t)j * c;
+        float v[VEC];
+        unpack16<T>(rv[u], v);
 #pragma unroll
-          for (int e = 0; e < VEC; e += 4) {
-            const float4 bz = __ldg(reinterpret_cast<const float4*>(bias + ch0 + e));
-            z[e] += bz.x; z[e + 1] += bz.y; z[e + 2] += bz.z; z[e + 3] += bz.w;
-          }
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            if (z[e] != -INFINITY) pool_update(z[e], v[e], mx[e], s[e], acc[e]);   // (weight 0)
-        }
+        for (int e = 0; e < VEC; ++e)
+          acc[e] = z[u][e] != 0.f ? fmaf(z[u][e], v[e], acc[e]) : acc[e];   // (a token of weight 0 is not read into the sum)
       }
     }
   }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) { st_mx[e][tid] = mx[e]; st_s[e][tid] = s[e]; st_acc[e][tid] = acc[e]; }
   __syncthreads();
-  // the first nv threads join the groups of their vector
-  float y[VEC];
+  // element x = e * nv + vec of the row by thread x mod kThreads: the groups'
+  // partials joined; the pooled values then go back through st_mx[e][vec]
   float ss = 0.f;
-  if (tid < nv) {
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float M = -INFINITY;
-      for (int g = 0; g < G; ++g) M = fmaxf(M, st_mx[e][g * nv + tid]);
-      float sum = 0.f, a = 0.f;
-      for (int g = 0; g < G; ++g) {
-        const float mg = st_mx[e][g * nv + tid];
-        const float f = mg == M ? 1.f : expf(mg - M); // (a group without tokens: expf(-inf) = 0)
-        sum = fmaf(st_s[e][g * nv + tid], f, sum);
-        a = fmaf(st_acc[e][g * nv + tid], f, a);
-      }
-      y[e] = a / sum;
-      ss = fmaf(y[e], y[e], ss);
+  for (int x = tid; x < VEC * nv; x += kThreads) {
+    const int e = x / nv, w = x - e * nv;
+    float M = -INFINITY;
+    for (int g = 0; g < G; ++g) M = fmaxf(M, st_mx[e][g * nv + w]);
+    float sum = 0.f, a = 0.f;
+    for (int g = 0; g < G; ++g) {
+      const float mg = st_mx[e][g * nv + w];
+      const float f = mg == M ? 1.f : exp2f(mg - M);  // (a group without tokens: exp2f(-inf) = 0)
+      sum = fmaf(st_s[e][g * nv + w], f, sum);
+      a = fmaf(st_acc[e][g * nv + w], f, a);
     }
+    const float r = a / sum;
+    st_mx[e][w] = r;                                  // (this thread alone reads column w of row e)
+    ss = fmaf(r, r, ss);
   }
+  float inv = 1.f;
   if (p.rms_norm) {
     ss = warp_sum(ss);
     if (lane == 0) red_s[tid >> 5] = ss;
     __syncthreads();
     float tot = 0.f;
-    for (int k = 0; k < (nv + 31) / 32; ++k) tot += red_s[k];
-    const float inv = rsqrtf(tot / (float)c + p.eps);
-    if (tid < nv) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) y[e] *= inv * (p.gain ? __ldg(p.gain + ch0 + e) : 1.f);
-    }
+    for (int k = 0; k < kThreads / 32; ++k) tot += red_s[k];
+    inv = rsqrtf(tot / (float)c + p.eps);
+  } else {
+    __syncthreads();
   }
+  float y[VEC];                                       // the first nv threads: a vector of the row
   if (tid < nv) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      y[e] = st_mx[e][tid] * (p.rms_norm ? inv * (p.gain ? __ldg(p.gain + ch0 + e) : 1.f) : 1.f);
     const int j0 = ch0 - (c - p.rope_dims);
 #pragma unroll
     for (int e = 0; e < VEC; e += 2) {

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   extern __shared__ __align__(16) uint8_t ts_smem[];
   int* idx_s = reinterpret_cast<int*>(ts_smem);                   // [k], -1 once pushed out
   float* sc_s = reinterpret_cast<float*>(idx_s + p.k);            // [k]
-  __shared__ int par_s[kTreeMaxNodes], path_s[kTreeMaxNodes], t_s;
+  __shared__ TreeNode node_s;
   __shared__ int dnode[kTreeMaxNodes], rank_s[kTreeMaxNodes], below[kTreeMaxNodes];
   __shared__ float dscore[kTreeMaxNodes], part_s[kTsThreads / 32];
   __shared__ int nd_s, valid_s, scan_s[kTsThreads / 32];
@@ -52,14 +52,13 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   griddep_wait();
   griddep_launch_dependents();
   const int node = blockIdx.x, b = node / p.T, i = node - b * p.T;
-  const int t = tree_node(p.parents, p.pos, b, p.T, i, par_s, path_s, &t_s);
+  const int t = tree_node(p.parents, p.pos, b, p.T, i, &node_s);
   if (t < 0) return;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) {
     int nd = 0;
-    const int p0 = p.pos[b];
-    for (int q = p0; q <= t; ++q)
-      if ((q + 1) % p.m == 0 && (q + 1) / p.m - 1 < p.N) dnode[nd++] = path_s[q - p0];
+    for (int q = node_s.pos0; q <= t; ++q)
+      if ((q + 1) % p.m == 0 && (q + 1) / p.m - 1 < p.N) dnode[nd++] = node_s.at(q);
     nd_s = nd;
     valid_s = 0;
   }
