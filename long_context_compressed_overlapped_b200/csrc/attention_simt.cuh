@@ -9,13 +9,8 @@
 // online softmax (max, sum) and each lane owns d/32 output dims, interleaved
 // so that the P.V reads are conflict-free too.  A split either writes the
 // final output (one split) or a partial (max, sum, acc) for the combine.
-//
-// kTree: the queries are draft-tree nodes; a node's keys are its selected
-// entries (CSA, drafted entries from index N on) or the committed entries
-// (HCA), then the rows of its plan's list (norm_rope.cuh).
 #pragma once
 #include "common.cuh"
-#include "norm_rope.cuh"
 
 namespace csahca {
 
@@ -41,28 +36,7 @@ struct SimtAttnParams {
   // outputs: partial == NULL -> final rows in out (one split); else partials
   void* out;                         // final [B, nq, H, d]
   float* partial;                    // [B, nq, H, splits, d + 4]: m, l, -, -, acc[d]
-  // kTree: rows of each code kind, the plan's lists [B, nq][list_stride] and per-node facts
-  const void* tree_rows[3];
-  const int* list; const int4* info; int list_stride;
 };
-
-// kTree: j counts the node's compressed keys, then its list (nullptr: no key).
-template <typename T>
-__device__ __forceinline__ const T* tree_key_row(const SimtAttnParams& p, int b, int qi, int j, int ncomp) {
-  if (j >= ncomp) {
-    const int code = p.list[((int64_t)b * p.nq + qi) * p.list_stride + (j - ncomp)];
-    const int kind = code >> kRowShift;
-    const void* base = kind == ROW_RING ? p.tree_rows[0] : kind == ROW_TREE ? p.tree_rows[1] : p.tree_rows[2];
-    return static_cast<const T*>(base) + (int64_t)(code & kRowMask) * p.d;
-  }
-  const int e = p.idx ? p.idx[((int64_t)b * p.nq + qi) * p.k + j] : j;
-  if (e < 0) return nullptr;
-  if (e < p.N) return static_cast<const T*>(p.kv_comp) + ((int64_t)b * p.N + e) * p.d;
-  if (e - p.N < p.nq && p.tree_rows[ROW_DRAFT])
-    return static_cast<const T*>(p.tree_rows[ROW_DRAFT]) + ((int64_t)b * p.nq + (e - p.N)) * p.d;
-  raise_device_error(DEVERR_BAD_INDEX);
-  return nullptr;
-}
 
 template <typename T>
 __device__ __forceinline__ const T* key_row(const SimtAttnParams& p, int b, int qi, int t,
@@ -78,7 +52,7 @@ __device__ __forceinline__ const T* key_row(const SimtAttnParams& p, int b, int 
   return static_cast<const T*>(p.win) + ((int64_t)b * p.nq + s) * p.d;
 }
 
-template <typename T, bool kTree = false>
+template <typename T>
 __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -91,10 +65,7 @@ __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams 
   const int qi = blockIdx.x % p.nq, b = blockIdx.x / p.nq;
   const int h = blockIdx.y * kSimtHG + wid;
   const int split = blockIdx.z;
-  int4 info = make_int4(0, 0, 0, 0);
-  if constexpr (kTree) info = p.info[blockIdx.x];
-  const int t = kTree ? info.x : p.decode ? p.pos[b] : qi;
-  if (kTree && t < 0) return;                       // no node: its rows are left as they are
+  const int t = p.decode ? p.pos[b] : qi;
   const int dpl = d / 32;
 
   // ---- query prologue: RMSNorm * gain, RoPE at t (lane owns dims lane + 32 e)
@@ -132,14 +103,13 @@ __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams 
   // ---- key list: compressed part then window part
   int ncomp;
   if (p.idx) ncomp = p.k;
-  else if (kTree) ncomp = info.y;
   else {
     int v = t < 0 ? 0 : (int)(((int64_t)t + 1) / p.m);
     ncomp = v < p.N ? v : p.N;
   }
   const int wlo = t - p.w + 1 > 0 ? t - p.w + 1 : 0;
   const int nwin = p.w > 0 ? t - wlo + 1 : 0;
-  const int J = ncomp + (kTree ? info.z : nwin);
+  const int J = ncomp + nwin;
   const int j0 = split * p.keys_per_split;
   const int j1 = min(J, j0 + p.keys_per_split);
 
@@ -152,9 +122,7 @@ __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams 
   for (int c0 = j0; c0 < j1; c0 += kSimtKeys) {
     const int nk = min(kSimtKeys, j1 - c0);
     if (threadIdx.x < kSimtKeys)
-      rows[threadIdx.x] = threadIdx.x >= nk ? nullptr
-                          : kTree ? tree_key_row<T>(p, b, qi, c0 + threadIdx.x, ncomp)
-                                  : key_row<T>(p, b, qi, t, c0 + threadIdx.x, ncomp, wlo);
+      rows[threadIdx.x] = threadIdx.x < nk ? key_row<T>(p, b, qi, t, c0 + threadIdx.x, ncomp, wlo) : nullptr;
     __syncthreads();
     for (int x = threadIdx.x; x < kSimtKeys * d; x += blockDim.x) {
       const int kk = x / d, dim = x % d;
@@ -198,9 +166,7 @@ __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams 
     const float z = p.sinks[h];
     const float M = fmaxf(mx, z);
     const float sc = (mx == -INFINITY) ? 0.f : expf(mx - M);
-    float den = expf(z - M) + lsum * sc;
-    // no key, or all weight on an infinite sink: o = 0
-    if (kTree && (mx == -INFINITY || z == INFINITY)) den = INFINITY;
+    const float den = expf(z - M) + lsum * sc;
     const int r0 = d - p.rope_dims;
     T* O = static_cast<T*>(p.out) + (((int64_t)b * p.nq + qi) * p.H + h) * d;
 #pragma unroll
@@ -233,7 +199,6 @@ struct CombineParams {
   void* out;
   int B, nq, H, d, splits, rope_dims, decode;
   double rope_base;
-  int tree;                   // rows of pos < 0 are left as they are; no key or an infinite sink gives 0
 };
 
 template <typename T>
@@ -248,16 +213,14 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(CombineParams p) {
   const int64_t bq = bqh / p.H;
   const int qi = (int)(bq % p.nq), b = (int)(bq / p.nq);
   const int t = p.decode ? p.pos[b] : qi;
-  if (p.tree && t < 0) return;
   const int64_t ps = p.d + 4;                       // partial row: m, l, -, -, acc[d]
   const float* P = p.partial + bqh * p.splits * ps;
   const float z = p.sinks[h];
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x;
-    float mk = -INFINITY;
-    for (int s = lane; s < p.splits; s += 32) mk = fmaxf(mk, P[(int64_t)s * ps]);
-    mk = warp_max(mk);
-    const float M = fmaxf(mk, z);
+    float M = z;
+    for (int s = lane; s < p.splits; s += 32) M = fmaxf(M, P[(int64_t)s * ps]);
+    M = warp_max(M);
     float den = 0.f;
     for (int s = lane; s < p.splits; s += 32) {
       const float ms = P[(int64_t)s * ps];
@@ -266,9 +229,8 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(CombineParams p) {
       den += P[(int64_t)s * ps + 1] * f;
     }
     den = warp_sum(den) + expf(z - M);
-    const bool none = p.tree && (mk == -INFINITY || z == INFINITY);
-    const float inv = none ? 0.f : 1.f / den;
-    for (int s = lane; s < p.splits; s += 32) wsplit[s] = none ? 0.f : wsplit[s] * inv;
+    const float inv = 1.f / den;
+    for (int s = lane; s < p.splits; s += 32) wsplit[s] *= inv;
   }
   __syncthreads();
   const int r0 = p.d - p.rope_dims;

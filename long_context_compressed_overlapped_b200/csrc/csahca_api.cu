@@ -29,6 +29,7 @@
 #include "tree_compress.cuh"
 #include "tree_select.cuh"
 #include "attention_tree_tc.cuh"
+#include "attention_tree_simt.cuh"
 
 using namespace csahca;
 
@@ -718,13 +719,13 @@ int launch_finish(const void* x, void* out, const float* gain, int64_t rows, int
   return CSAHCA_OK;
 }
 
-template <typename T, bool kTree = false>
+template <typename T>
 int launch_simt_attn(const SimtAttnParams& p, int nq_total, cudaStream_t s, const char* name) {
   const size_t smem = ((size_t)kSimtHG * p.d + (size_t)kSimtKeys * (p.d + 1)) * sizeof(float);
-  cudaFuncSetAttribute(attn_simt_kernel<T, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaFuncSetAttribute(attn_simt_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   dim3 grid((unsigned)nq_total, (unsigned)ceil_div64(p.H, kSimtHG), (unsigned)p.splits);
   CSAHCA_TRACE(name, s);
-  launch_k(attn_simt_kernel<T, kTree>, dim3(grid), dim3(32 * kSimtHG), smem, s, p);
+  launch_k(attn_simt_kernel<T>, dim3(grid), dim3(32 * kSimtHG), smem, s, p);
   CSAHCA_CHECK_LAUNCH();
   return CSAHCA_OK;
 }
@@ -1105,7 +1106,7 @@ int run_decode_t(const csahca_decode_args* a, cudaStream_t s, char* ws) {
   CombineParams c;
   c.partial = partial; c.sinks = a->sinks; c.pos = a->pos; c.out = a->out;
   c.B = a->B; c.nq = 1; c.H = a->H; c.d = a->d; c.splits = L.splits;
-  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base; c.tree = 0;
+  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base;
   {
     CSAHCA_TRACE("attn_combine", s);
     launch_k(attn_combine_kernel<T>, dim3((unsigned)(a->B * a->H)), dim3(128), 0, s, c);
@@ -1453,9 +1454,9 @@ int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
   if (a->B < 0 || a->T < 0 || a->H < 1 || a->d < 1 || a->N_cap < 0 || a->m < 1 || a->w < 0)
     return CSAHCA_ERR_INVALID_ARG;
   if (a->rope_dims < 0 || a->rope_dims > a->d || (a->rope_dims & 1)) return CSAHCA_ERR_INVALID_ARG;
-  if (a->T > CSAHCA_TREE_MAX_NODES || a->d % 32 || a->d > 32 * kSimtMaxDPL) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->T > CSAHCA_TREE_MAX_NODES || a->d % 32 || a->d > 512) return CSAHCA_ERR_UNSUPPORTED;
   // row codes and tensor coordinates are 32-bit
-  if ((int64_t)a->B * a->T * a->H > INT32_MAX || (int64_t)a->B * a->N_cap > INT32_MAX ||
+  if ((int64_t)a->B * a->T * a->H > INT32_MAX || a->H > 65535 || (int64_t)a->B * a->N_cap > INT32_MAX ||
       (int64_t)a->B * a->w > kRowMask || (int64_t)a->B * a->T > kRowMask)
     return CSAHCA_ERR_UNSUPPORTED;
   const bool csa = a->kind == CSAHCA_CSA;
@@ -1490,7 +1491,7 @@ int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
 struct TreeLayout {
   size_t node_pos, sel_pos, info, list, rows, q, sel_scores, idx, indexer, indexer_bytes, partial, total;
   bool tc;
-  int splits, keys_per_split;
+  int splits;
 };
 
 // Splits of a node's tiles: `nodes` x s items over the SMs in waves, an item
@@ -1533,20 +1534,21 @@ TreeLayout tree_layout(const csahca_tree_attn_args* a) {
     take(L.indexer_bytes);
   }
   const int64_t jmax = (csa ? (int64_t)a->k : (int64_t)a->N_cap) + a->w + (csa ? 0 : a->T);
-  L.keys_per_split = 0;
   if (L.tc) {
     const int64_t tiles = csa ? ceil_div64((int64_t)a->k + a->w, kTreeTile)
                               : a->N_cap / kTreeTile + ceil_div64((int64_t)(a->N_cap % kTreeTile) + a->w, kTreeTile);
     L.splits = tree_splits(nodes, (int)(tiles > 0 ? tiles : 1));
     L.partial = L.splits > 1 ? take((size_t)nodes * L.splits * kTreePartialBytes) : off;
   } else {
-    const int64_t ctas = nodes * ceil_div64(a->H, kSimtHG);
-    int64_t s = ceil_div64(4 * num_sms(), ctas > 0 ? ctas : 1);
-    const int64_t most = jmax > 0 ? ceil_div64(jmax, 128) : 1;
+    // splits where the CTAs of one split leave SMs idle and each would still
+    // take a few tiles a warp (joining costs a launch, about two tiles' time)
+    const int64_t ctas = nodes * ceil_div64(a->H, kTsaHeads);
+    const int64_t round = (int64_t)tsa_warps((int)ceil_div64(a->d, 32)) * kTsaKeys;
+    int64_t s = ceil_div64(2 * num_sms(), ctas > 0 ? ctas : 1);
+    const int64_t most = jmax / (2 * round);
     if (s > most) s = most;
-    if (s > kCombineMaxSplits) s = kCombineMaxSplits;
+    if (s > kTsaMaxSplits) s = kTsaMaxSplits;
     L.splits = (int)(s < 1 ? 1 : s);
-    L.keys_per_split = (int)(jmax > 0 ? ceil_div64(jmax, L.splits) : 1);
     L.partial = L.splits > 1 ? take((size_t)nodes * a->H * L.splits * (a->d + 4) * 4) : off;
   }
   L.total = off;
@@ -1608,6 +1610,16 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     CSAHCA_CHECK_LAUNCH();
   }
   return CSAHCA_OK;
+}
+
+template <typename T, int DPL>
+void launch_tree_simt(const TreeSimtParams& p, int nodes, cudaStream_t s) {
+  constexpr int warps = tsa_warps(DPL);
+  const int smem = (kTsaHeads * p.d + warps * kTsaKeys * (p.d + 4)) * (int)sizeof(float);
+  cudaFuncSetAttribute(attn_tree_simt_kernel<T, DPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  CSAHCA_TRACE(p.idx ? "attn_tree_csa_simt" : "attn_tree_hca_simt", s);
+  launch_k(attn_tree_simt_kernel<T, DPL>, dim3((unsigned)nodes, (unsigned)ceil_div64(p.H, kTsaHeads), (unsigned)p.splits),
+           dim3(32 * warps), smem, s, p);
 }
 
 template <typename T>
@@ -1680,26 +1692,27 @@ int run_tree_t(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws, cu
   if constexpr (sizeof(T) == 2) {
     if (L.tc) return launch_tree_tc(a, L, ws, sel, scale, base, s);
   }
-  SimtAttnParams p;
+  TreeSimtParams p;
   memset(&p, 0, sizeof(p));
-  p.q = a->q; p.q_gain = a->q_gain; p.sinks = a->sinks; p.pos = node_pos;
-  p.q_norm = a->q_norm; p.eps = eps; p.scale = scale; p.rope_dims = a->rope_dims; p.rope_base = base;
-  p.B = a->B; p.nq = a->T; p.H = a->H; p.d = a->d;
-  p.kv_comp = a->kv_cache; p.N = a->N_cap; p.idx = sel; p.k = a->k; p.m = a->m; p.w = a->w;
-  p.splits = L.splits; p.keys_per_split = L.keys_per_split;
-  p.out = a->out; p.partial = L.splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
-  p.tree_rows[ROW_RING] = a->win; p.tree_rows[ROW_TREE] = ws + L.rows; p.tree_rows[ROW_DRAFT] = a->draft;
+  p.q = a->q; p.q_gain = a->q_gain; p.sinks = a->sinks;
+  p.q_norm = a->q_norm; p.eps = eps; p.scale = scale; p.rope_dims = a->rope_dims;
+  p.T = a->T; p.H = a->H; p.d = a->d;
+  p.kv = a->kv_cache; p.N = a->N_cap; p.idx = sel; p.k = a->k;
+  p.rows[ROW_RING] = a->win; p.rows[ROW_TREE] = ws + L.rows; p.rows[ROW_DRAFT] = a->draft;
   p.list = list; p.info = info; p.list_stride = a->w + a->T;
-  st = launch_simt_attn<T, true>(p, nodes, s, csa ? "attn_tree_csa_simt" : "attn_tree_hca_simt");
-  if (st != CSAHCA_OK || L.splits == 1) return st;
-  CombineParams c;
-  memset(&c, 0, sizeof(c));
-  c.partial = p.partial; c.sinks = a->sinks; c.pos = node_pos; c.out = a->out;
-  c.B = nodes; c.nq = 1; c.H = a->H; c.d = a->d; c.splits = L.splits;
-  c.rope_dims = a->rope_dims; c.decode = 1; c.rope_base = base; c.tree = 1;
+  p.splits = L.splits; p.out = a->out;
+  p.partial = L.splits > 1 ? reinterpret_cast<float*>(ws + L.partial) : nullptr;
+  rope_theta_pairs(p.theta, a->rope_dims, base);
+  const int dpl = a->d / 32;
+  if (dpl <= 2) launch_tree_simt<T, 2>(p, nodes, s);
+  else if (dpl <= 4) launch_tree_simt<T, 4>(p, nodes, s);
+  else if (dpl <= 8) launch_tree_simt<T, 8>(p, nodes, s);
+  else launch_tree_simt<T, 16>(p, nodes, s);
+  CSAHCA_CHECK_LAUNCH();
+  if (L.splits == 1) return CSAHCA_OK;
   {
     CSAHCA_TRACE("attn_tree_combine", s);
-    launch_k(attn_combine_kernel<T>, dim3((unsigned)(nodes * a->H)), dim3(128), 0, s, c);
+    launch_k(tree_simt_combine_kernel<T>, dim3((unsigned)(nodes * a->H)), dim3(128), 0, s, p);
   }
   CSAHCA_CHECK_LAUNCH();
   return CSAHCA_OK;

@@ -108,6 +108,7 @@ INDEXER = dict(idx_in=None, HI=4, dI=128, qI_dtype=N.BF16, kI_dtype=N.BF16, qI=6
     (dict(k=2**31 - 1), N.ERR_UNSUPPORTED),
     (dict(N_cap=2**31 - 1), N.ERR_UNSUPPORTED),
     (dict(w=1 << 28), N.ERR_UNSUPPORTED),
+    (dict(H=65536), N.ERR_UNSUPPORTED),
     (dict(q=None), N.ERR_INVALID_ARG),
     (dict(out=64), N.ERR_INVALID_ARG),                                              # out is q
     (dict(parents=None), N.ERR_INVALID_ARG),
