@@ -65,6 +65,7 @@ struct TreeAttnParams {
   const __nv_bfloat16* rows[3];          // ROW_RING, ROW_TREE, ROW_DRAFT bases
   const int* idx;                        // CSA: [nodes, k]; null: HCA
   const int* list; const int4* info;
+  const float2* turn;                    // [nodes][rope_dims / 2] cos, sin of the node's angles
   const float* sinks;
   int list_stride;                       // w + T
   int k, N, T;
@@ -73,7 +74,6 @@ struct TreeAttnParams {
   int rope_dims;
   __nv_bfloat16* out;                    // [nodes, H, D]
   char* partial;                         // [nodes][splits] blocks of kTreePartialBytes
-  double theta[64];
 };
 
 struct TreeItem { int node, split, t, full, tail, nlist, tile0, tile1; };
@@ -186,7 +186,6 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
   __shared__ __align__(16) float red[2][4][32];
   __shared__ __align__(16) float stat_a[kAttnH];
   __shared__ float m_run[kAttnH], l_run[kAttnH];
-  __shared__ double theta_s[64];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kWarpS = 8 + kTreeProducers, kWarpPV = kWarpS + 1;
@@ -206,7 +205,6 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     mbar_init(&bar_done, 2);
     mbar_fence_init();
   }
-  if (threadIdx.x < 64) theta_s[threadIdx.x] = p.theta[threadIdx.x];
   if (warp == kWarpS) tmem_alloc(&tmem_base_sh, 512);
   tc_fence_before();
   __syncthreads();
@@ -412,12 +410,18 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     const int wq = warp & 3;
     const int key0 = 16 * wq + (lane >> 2);              // this thread's keys: key0, key0 + 8
     const int hl = 2 * (lane & 3);                       // its heads: h0 + 8 j + hl + {0, 1}, j = 0 .. 3
+    const float z2 = p.sinks[h0 + lane] * kLog2e;        // (of head h0 + lane)
     int4 f = tree_info(p, blockIdx.x);
     for (int id = blockIdx.x; id < p.n_items; id += gridDim.x) {
       const TreeItem it = tree_item(p, id, f);
       f = tree_info(p, id + gridDim.x);
       const bool empty = it.tile1 <= it.tile0;
       bool bad = false;                      // uniform over the group; both groups leave together
+      // this thread's dim of the last M-tile turns back by this angle (rope_dims <= 128)
+      float2 turn = make_float2(1.f, 0.f);
+      const bool rot = 3 * 128 + tid >= r0;
+      if (rot && it.t >= 0 && p.splits == 1)
+        turn = __ldg(p.turn + (int64_t)it.node * (p.rope_dims >> 1) + ((3 * 128 + tid - r0) >> 1));
       float m[8], l[8];                      // [2 j + {0, 1}]: running max (log2 units) and this thread's share of the sum
 #pragma unroll
       for (int x = 0; x < 8; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
@@ -590,11 +594,12 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
             }
           }
         } else {
-          // o = O / (l + e^{z - m}), rope dims rotated back by -t
-          __nv_bfloat16* O = p.out + (int64_t)it.node * kAttnH * kAttnD;
+          // o = O / (l + e^{z - m}), rope dims rotated back by -t.  A thread
+          // stores its dim of each head, a warp 64 contiguous bytes (two whole
+          // sectors): turning the tile through shared memory first took 9,000
+          // cycles an item, most of them cold instructions and barriers
           if (tid < 32) {                    // (this warp wrote l_run; m_run: see the barrier above)
             const int h = h0 + tid;
-            const float z2 = p.sinks[h] * kLog2e;
             const float mu = empty ? -INFINITY : m_run[h];
             const float M = fmaxf(mu, z2);
             const float den = exp2f(z2 - M) + (mu == -INFINITY ? 0.f : l_run[h] * exp2f(mu - M));
@@ -602,15 +607,10 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
             stat_a[h] = (mu == -INFINITY || z2 == INFINITY) ? 0.f : exp2f(mu - M) / den;
           }
           group_sync(gid);
-          __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sP) + g * 32 * 128;   // [32 heads][128 dims]
           const float4* fac4 = reinterpret_cast<const float4*>(stat_a + h0);
+          __nv_bfloat16* O = p.out + ((int64_t)it.node * kAttnH + h0) * kAttnD + tid;
 #pragma unroll 1
           for (int mt = 0; mt < kAttnMT; ++mt) {
-            const int dim = mt * 128 + tid;
-            const bool mt_rope = mt * 128 + 127 >= r0;
-            const bool rot = dim >= r0;
-            float cs = 1.f, sn = 0.f;
-            if (rot) rope_sincos(-(double)it.t, theta_s[(dim - r0) >> 1], &cs, &sn);
             float o[32];
             if (!empty) {
               tmem_ld32(tO + lane_base + mt * kAttnH + h0, o);
@@ -624,24 +624,16 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
               const float4 fc = fac4[e4];
               o[e4 * 4 + 0] *= fc.x; o[e4 * 4 + 1] *= fc.y; o[e4 * 4 + 2] *= fc.z; o[e4 * 4 + 3] *= fc.w;
             }
-            if (mt_rope) {
+            if (mt == kAttnMT - 1 && r0 < kAttnD) {
+              // pair partners are neighbouring lanes
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 const float partner = __shfl_xor_sync(0xffffffffu, o[e], 1);
-                if (rot) o[e] = (dim & 1) ? fmaf(partner, sn, o[e] * cs) : fmaf(-partner, sn, o[e] * cs);
+                if (rot) o[e] = (tid & 1) ? fmaf(-partner, turn.y, o[e] * turn.x) : fmaf(partner, turn.y, o[e] * turn.x);
               }
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) stage[e * 128 + tid] = __float2bfloat16_rn(o[e]);
-            group_sync(gid);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int pc = tid + 128 * i;                // 16-byte piece: head pc / 16
-              const int h = pc >> 4, off = (pc & 15) * 8;
-              const uint4 val = *reinterpret_cast<const uint4*>(stage + h * 128 + off);
-              *reinterpret_cast<uint4*>(O + (int64_t)(h0 + h) * kAttnD + mt * 128 + off) = val;
-            }
-            group_sync(gid);
+            for (int e = 0; e < 32; ++e) O[(int64_t)e * kAttnD + mt * 128] = __float2bfloat16_rn(o[e]);
           }
         }
       }

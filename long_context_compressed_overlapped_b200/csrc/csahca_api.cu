@@ -1489,7 +1489,7 @@ int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
 }
 
 struct TreeLayout {
-  size_t node_pos, sel_pos, info, list, rows, q, sel_scores, idx, indexer, indexer_bytes, partial, total;
+  size_t node_pos, sel_pos, info, turn, list, rows, q, sel_scores, idx, indexer, indexer_bytes, partial, total;
   bool tc;
   int splits;
 };
@@ -1520,6 +1520,7 @@ TreeLayout tree_layout(const csahca_tree_attn_args* a) {
   L.node_pos = take(nodes * 4);
   L.sel_pos = take(nodes * 4);
   L.info = take(nodes * 16);
+  L.turn = L.tc ? take((size_t)nodes * (a->rope_dims / 2) * 8) : off;
   L.list = take((size_t)nodes * (a->w + a->T) * 4);
   L.rows = take(nodes * a->d * e);
   L.q = L.tc ? take((size_t)nodes * a->H * a->d * e) : off;
@@ -1566,10 +1567,10 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   p.rows[ROW_TREE] = reinterpret_cast<const __nv_bfloat16*>(ws + L.rows);
   p.rows[ROW_DRAFT] = static_cast<const __nv_bfloat16*>(a->draft);
   p.idx = sel; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
+  p.turn = reinterpret_cast<const float2*>(ws + L.turn);
   p.sinks = a->sinks; p.list_stride = a->w + a->T; p.k = a->k; p.N = a->N_cap; p.T = a->T;
   p.splits = L.splits; p.n_items = nodes * L.splits; p.scale_log2 = scale * kLog2e; p.rope_dims = a->rope_dims;
   p.out = static_cast<__nv_bfloat16*>(a->out); p.partial = ws + L.partial;
-  rope_theta_pairs(p.theta, a->rope_dims, base);              // (the rest stays zero)
   // rows of 512 bf16 as [chunk 8][row][64]: a key box is four chunks of 64
   // rows (32 KB), the query box all 8 chunks of a node's 64 heads
   CUtensorMap m_rows, m_q;
@@ -1604,7 +1605,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     memset(&c, 0, sizeof(c));
     c.partial = p.partial; c.sinks = a->sinks; c.node_pos = reinterpret_cast<const int*>(ws + L.node_pos);
     c.out = p.out; c.splits = L.splits; c.rope_dims = a->rope_dims;
-    memcpy(c.theta, p.theta, sizeof(c.theta));
+    rope_theta_pairs(c.theta, a->rope_dims, base);            // (the rest stays zero)
     CSAHCA_TRACE("attn_tree_combine", s);
     launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / kTreeCombineDims), dim3(kTreeCombineThreads), 0, s, c);
     CSAHCA_CHECK_LAUNCH();
@@ -1655,6 +1656,7 @@ int run_tree_t(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws, cu
     t.parents = a->parents; t.pos = a->pos; t.T = a->T; t.w = a->w; t.m = a->m; t.N = a->N_cap;
     t.list_drafts = !csa && a->draft ? 1 : 0;
     t.node_pos = node_pos; t.sel_pos = sel_pos; t.list = list; t.info = info;
+    t.turn = L.tc ? reinterpret_cast<float2*>(ws + L.turn) : nullptr;
     rope_theta_pairs(p.theta, a->rope_dims, base);
     st = launch_norm_rope<T, true>(p, nodes, s);
     if (st != CSAHCA_OK) return st;

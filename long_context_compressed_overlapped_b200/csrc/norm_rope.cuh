@@ -45,6 +45,7 @@ struct TreePlan {
   int* sel_pos;             // [B, T] pos - 1 (the committed tokens' last position), -1: no node
   int* list;                // [B, T][w + T] row codes
   int4* info;               // [B, T] {position, visible committed entries, length of the list, 0}
+  float2* turn;             // [B, T][r / 2] cos, sin of the node's angles (optional)
 };
 
 struct NormRopeParams {
@@ -257,6 +258,9 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
         float2 c;
         rope_sincos((double)pos_s[q], p.theta[j - q * npair], &c.x, &c.y);
         cs_s[j] = c;
+        if constexpr (kTree) {
+          if (p.plan.turn && blockIdx.y == 0) p.plan.turn[(int64_t)tok0 * npair + j] = c;
+        }
       }
       __syncthreads();
       have_cs = true;
