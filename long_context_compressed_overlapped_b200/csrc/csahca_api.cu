@@ -467,6 +467,16 @@ bool decode_route_ok(const csahca_indexer_args* a) {
   return a->B * sp <= num_sms() && tps <= kRouteMaxTiles;
 }
 
+// Items that share a query tile's key tiles when `items` query tiles (a chunk of
+// several queries) are fewer than the SMs: as many as fill one wave, each with
+// at least four tiles (512 keys).
+int query_splits(const csahca_indexer_args* a, int items) {
+  int s = items > 0 ? num_sms() / items : 1;
+  const int most = (int)ceil_div64(a->N, 4 * 128);
+  if (s > most) s = most;
+  return s < 1 ? 1 : s;
+}
+
 int launch_indexer_tc(const csahca_indexer_args* a, int q0, int qc, float* scores, int64_t stride,
                       cudaStream_t s, uint32_t* hist = nullptr, uint32_t* counters = nullptr, int* above = nullptr,
                       uint2* cand = nullptr) {
@@ -480,6 +490,7 @@ int launch_indexer_tc(const csahca_indexer_args* a, int q0, int qc, float* score
   p.scores = scores; p.score_row_stride = stride;
   p.B = a->B; p.nq = a->nq; p.HI = a->HI; p.N = a->N; p.m = a->m; p.entry_base = a->entry_base;
   p.q_begin = q0; p.q_count = qc;
+  p.qsplits = 1;
   if (a->k_dtype == CSAHCA_E4M3) {
     // e4m3 keys straight into the FP8 tensor cores, one query per work item;
     // decode spreads each sequence's key tiles over about one CTA per SM
@@ -488,9 +499,10 @@ int launch_indexer_tc(const csahca_indexer_args* a, int q0, int qc, float* score
       p.n_items = a->B * p.splits;
     } else {
       p.splits = 0;
-      p.n_items = a->B * qc;
+      p.qsplits = query_splits(a, a->B * qc);
+      p.n_items = a->B * qc * p.qsplits;
     }
-    p.items_per_row = p.splits > 0 ? p.splits : 1;
+    p.items_per_row = p.splits > 0 ? p.splits : p.qsplits;
     p.route = above != nullptr ? 1 : 0;
     p.above = above;
     p.cand = cand;
@@ -529,7 +541,8 @@ int launch_indexer_tc(const csahca_indexer_args* a, int q0, int qc, float* score
     return launch_indexer_tc_t<1, false>(a, p, s);
   }
   p.splits = 0;
-  p.n_items = a->B * (int)ceil_div64(qc, 4);
+  p.qsplits = query_splits(a, a->B * (int)ceil_div64(qc, 4));
+  p.n_items = a->B * (int)ceil_div64(qc, 4) * p.qsplits;
   return launch_indexer_tc_t<4, false>(a, p, s);
 }
 

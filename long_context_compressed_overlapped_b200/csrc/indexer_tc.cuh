@@ -50,6 +50,9 @@ struct IdxTcParams {
   int route;
   int* above;
   uint2* cand;
+  // prefill items: each query tile's key tiles over qsplits items (1: whole
+  // rows), for calls of few queries, whose rows would leave most SMs idle
+  int qsplits;
 };
 
 // ---- fused top-k routing (decode; the histogram and counters of
@@ -227,6 +230,8 @@ __device__ __forceinline__ IdxItem idx_item(const IdxTcParams& p, int id) {
     it.kt1 = min(nt, it.kt0 + p.tiles_per_split);
   } else {
     const int nqt = (p.q_count + QT - 1) / QT;
+    const int sp = id % p.qsplits;
+    id /= p.qsplits;
     const int r = id / p.B;
     it.b = id % p.B;
     const int qt = nqt - 1 - r;                       // longest (latest) query tiles first
@@ -234,8 +239,9 @@ __device__ __forceinline__ IdxItem idx_item(const IdxTcParams& p, int id) {
     it.qn = min(QT, p.q_begin + p.q_count - it.q0);
     int vmax = 0;
     for (int q = 0; q < it.qn; ++q) vmax = max(vmax, idx_visible(p, it.b, it.q0 + q));
-    it.kt0 = 0;
-    it.kt1 = (vmax + 127) / 128;
+    const int nt = (vmax + 127) / 128;
+    it.kt0 = (int)((int64_t)nt * sp / p.qsplits);
+    it.kt1 = (int)((int64_t)nt * (sp + 1) / p.qsplits);
   }
   return it;
 }
