@@ -651,11 +651,13 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
 // Join of a node's splits with the sink, and the output de-rotation:
 // o = sum_s f_s (O_s / l_s), f_s = l_s 2^(m_s - M) / (2^(z - M) + sum_s l_s 2^(m_s - M)).
 // One CTA per (node, 32 dims).  The partials are in L2; each thread reads its
-// dim pair's 4 heads of four splits at a time, so the kernel is two or three
-// L2 round trips.
+// dim pair's 4 heads of four splits at a time, the first ones together with the
+// headers, so that a few splits cost one round trip (10 us with the position,
+// the maxima, the sums and O read one after another).
 constexpr int kTreeCombineDims = 32;
 constexpr int kTreeCombineThreads = 256;
 constexpr int kTreeMaxSplits = 148;
+__host__ __device__ constexpr int tree_combine_smem(int splits) { return splits * 2 * kAttnH * 4; }
 
 struct TreeCombineParams {
   const char* partial; const float* sinks; const int* node_pos;
@@ -665,59 +667,73 @@ struct TreeCombineParams {
 };
 
 __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const __grid_constant__ TreeCombineParams p) {
-  __shared__ __align__(16) float w_s[kTreeMaxSplits][kAttnH];
+  extern __shared__ __align__(16) float cmb_s[];
+  float (*w_s)[kAttnH] = reinterpret_cast<float (*)[kAttnH]>(cmb_s);
+  float (*l_s)[kAttnH] = w_s + p.splits;
   __shared__ __align__(16) __nv_bfloat16 stage[kAttnH][kTreeCombineDims + 8];
-  __shared__ float red[4][kAttnH];
+  __shared__ float red[4][kAttnH], red2[4][kAttnH];
   griddep_wait();
   griddep_launch_dependents();
   const int node = blockIdx.x, d0 = blockIdx.y * kTreeCombineDims;
-  const int t = p.node_pos[node];
-  if (t < 0) return;
   const int tid = threadIdx.x;
   const float* P = reinterpret_cast<const float*>(p.partial) + (int64_t)node * p.splits * kTreePartialFloats;
-  // weights: thread (head h, part) takes the splits part, part + 4, ...
-  {
-    const int h = tid & 63, part = tid >> 6;
-    const float z2 = p.sinks[h] * kLog2e;
-    float mx = -INFINITY;
-    for (int s = part; s < p.splits; s += 4) {
-      const float m = P[(int64_t)s * kTreePartialFloats + h];
-      w_s[s][h] = m;
-      mx = fmaxf(mx, m);
-    }
-    red[part][h] = mx;
-    __syncthreads();
-    const float mk = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
-    const float M = fmaxf(mk, z2);
-    float den = 0.f;
-    for (int s = part; s < p.splits; s += 4) {
-      const float m = w_s[s][h];
-      const float f = m == -INFINITY ? 0.f : P[(int64_t)s * kTreePartialFloats + kAttnH + h] * exp2f(m - M);
-      w_s[s][h] = f;
-      den += f;
-    }
-    __syncthreads();
-    red[part][h] = den;
-    __syncthreads();
-    den = red[0][h] + red[1][h] + red[2][h] + red[3][h] + exp2f(z2 - M);
-    // no key, or all weight on an infinite sink: o = 0
-    const float inv = (mk == -INFINITY || z2 == INFINITY) ? 0.f : 1.f / den;
-    for (int s = part; s < p.splits; s += 4) {
-      const float f = w_s[s][h];
-      w_s[s][h] = f > 0.f ? f * inv : 0.f;
-    }
-  }
-  __syncthreads();
   const int dp = tid >> 4, h4 = (tid & 15) * 4;          // dims d0 + 2 dp, + 1; heads h4 .. h4 + 3
   const float* src = P + 2 * kAttnH + (d0 + 2 * dp) * kAttnH + h4;
+  // the position, the headers and the first splits' O are asked for together
+  // (the partial blocks of a place without a node hold no numbers, but exist)
+  const int t = p.node_pos[node];
+  const int h = tid & 63, part = tid >> 6;
+  const float z2 = p.sinks[h] * kLog2e;
+  float4 x[4], y[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (u < p.splits) {
+      x[u] = *reinterpret_cast<const float4*>(src + (int64_t)u * kTreePartialFloats);
+      y[u] = *reinterpret_cast<const float4*>(src + (int64_t)u * kTreePartialFloats + kAttnH);
+    }
+  }
+  // weights: thread (head h, part) takes the splits part, part + 4, ...
+  float mx = -INFINITY;
+#pragma unroll 4
+  for (int s = part; s < p.splits; s += 4) {
+    const float m = P[(int64_t)s * kTreePartialFloats + h];
+    l_s[s][h] = P[(int64_t)s * kTreePartialFloats + kAttnH + h];
+    w_s[s][h] = m;
+    mx = fmaxf(mx, m);
+  }
+  if (t < 0) return;
+  red[part][h] = mx;
+  __syncthreads();
+  const float mk = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
+  const float M = fmaxf(mk, z2);
+  float den = 0.f;
+  for (int s = part; s < p.splits; s += 4) {
+    const float m = w_s[s][h];
+    const float f = m == -INFINITY ? 0.f : l_s[s][h] * exp2f(m - M);
+    w_s[s][h] = f;
+    den += f;
+  }
+  red2[part][h] = den;
+  __syncthreads();
+  // each thread's four heads: 1 / den (0: no key, or all weight on an infinite sink)
+  float inv[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int hh = h4 + e;
+    const float ze = p.sinks[hh] * kLog2e;
+    const float mke = fmaxf(fmaxf(red[0][hh], red[1][hh]), fmaxf(red[2][hh], red[3][hh]));
+    const float de = red2[0][hh] + red2[1][hh] + red2[2][hh] + red2[3][hh] + exp2f(ze - fmaxf(mke, ze));
+    inv[e] = (mke == -INFINITY || ze == INFINITY) ? 0.f : 1.f / de;
+  }
   float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s0 = 0; s0 < p.splits; s0 += 4) {
-    float4 x[4], y[4];
+    if (s0 > 0) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (s0 + u < p.splits) {
-        x[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats);
-        y[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats + kAttnH);
+      for (int u = 0; u < 4; ++u) {
+        if (s0 + u < p.splits) {
+          x[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats);
+          y[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats + kAttnH);
+        }
       }
     }
 #pragma unroll
@@ -729,12 +745,14 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // (a split of weight 0 may hold no O: its bytes are not used)
-          a0[e] += ws[e] != 0.f ? ws[e] * xs[e] : 0.f;
-          a1[e] += ws[e] != 0.f ? ws[e] * ys[e] : 0.f;
+          a0[e] += ws[e] > 0.f ? ws[e] * xs[e] : 0.f;
+          a1[e] += ws[e] > 0.f ? ws[e] * ys[e] : 0.f;
         }
       }
     }
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) { a0[e] = inv[e] != 0.f ? a0[e] * inv[e] : 0.f; a1[e] = inv[e] != 0.f ? a1[e] * inv[e] : 0.f; }
   const int j0 = d0 + 2 * dp - (kAttnD - p.rope_dims);
   if (j0 >= 0) {
     float cs, sn;
@@ -750,9 +768,9 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
   for (int e = 0; e < 4; ++e)
     *reinterpret_cast<__nv_bfloat162*>(&stage[h4 + e][2 * dp]) = __floats2bfloat162_rn(a0[e], a1[e]);
   __syncthreads();
-  const int h = tid >> 2, pc = (tid & 3) * 8;
-  *reinterpret_cast<uint4*>(p.out + ((int64_t)node * kAttnH + h) * kAttnD + d0 + pc) =
-      *reinterpret_cast<const uint4*>(&stage[h][pc]);
+  const int ho = tid >> 2, pc = (tid & 3) * 8;
+  *reinterpret_cast<uint4*>(p.out + ((int64_t)node * kAttnH + ho) * kAttnD + d0 + pc) =
+      *reinterpret_cast<const uint4*>(&stage[ho][pc]);
 }
 
 }  // namespace csahca

@@ -1620,7 +1620,10 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     c.out = p.out; c.splits = L.splits; c.rope_dims = a->rope_dims;
     rope_theta_pairs(c.theta, a->rope_dims, base);            // (the rest stays zero)
     CSAHCA_TRACE("attn_tree_combine", s);
-    launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / kTreeCombineDims), dim3(kTreeCombineThreads), 0, s, c);
+    const int smem = tree_combine_smem(L.splits);
+    if (smem > 32 * 1024)
+      cudaFuncSetAttribute(tree_combine_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    launch_k(tree_combine_kernel, dim3((unsigned)nodes, kAttnD / kTreeCombineDims), dim3(kTreeCombineThreads), smem, s, c);
     CSAHCA_CHECK_LAUNCH();
   }
   return CSAHCA_OK;

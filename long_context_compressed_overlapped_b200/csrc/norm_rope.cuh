@@ -109,6 +109,15 @@ template <> __device__ __forceinline__ void unpack16<__nv_bfloat16>(const uint4&
   }
 }
 
+// The positions at which a path completes stored entries: from the first
+// block end at or after pos0, every m, up to the last one <= t whose entry is < N.
+// (64-bit: a step past a position near 2^31 must not wrap)
+__device__ __forceinline__ int64_t tree_first_end(int pos0, int m) { return (int64_t)pos0 + (m - 1 - pos0 % m); }
+__device__ __forceinline__ int tree_entries_end(int t, int m, int N) {
+  const int64_t last = (int64_t)N * m - 1;          // the block end of entry N - 1
+  return last < t ? (int)last : t;
+}
+
 // Pairs of fp32 in one 64-bit register.
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
   uint64_t r;
@@ -175,6 +184,47 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
   const int heads = p.heads[0] + p.heads[1];
   const int npair = p.rope_dims >> 1;
 
+  // rows of this CTA: [row_begin, row_end) of one token, or all of tpc tokens
+  const int row_begin = blockIdx.y * p.rows_per_cta;
+  const int row_end = p.tpc > 1 ? heads : min(heads, row_begin + p.rows_per_cta);
+  const int n_rows = p.tpc > 1 ? p.tpc * heads : row_end - row_begin;
+  const int nch = p.d / VEC;
+  int tk = 0, row = row_begin + slot;                 // this lane group's next row
+  if (p.tpc > 1) { tk = slot / heads; row = slot - tk * heads; }
+  const int step_t = p.tpc > 1 ? RPC / heads : 0, step_r = RPC - step_t * heads;
+  bool have_cs = false;
+  int which = -1;
+  uint64_t gain[NCH][V2];
+  uint4 raw[U][NCH];
+  T* out[U];
+  int ut[U];                                          // token of the row (-1: nothing to do)
+  bool uk[U];
+  const auto load_turn = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = r0 + u * RPC + slot < n_rows && (kTree || pos_s[tk] >= 0);
+      const int k = row >= p.heads[0];
+      ut[u] = in ? tk : -1;
+      uk[u] = k;
+      if (in) {
+        const int h = row - k * p.heads[0];
+        const int64_t xo = kTree ? (int64_t)tok0 * p.xs[k][1] : off_s[k][tk];
+        const int64_t yo = kTree ? (int64_t)tok0 * p.ys[k][1] : off_s[2 + k][tk];
+        const T* x = static_cast<const T*>(p.x[k]) + (xo + h * p.xs[k][2] + sub * VEC);
+        out[u] = static_cast<T*>(p.y[k]) + (yo + h * p.d + sub * VEC);
+#pragma unroll
+        for (int q = 0; q < NCH; ++q) {
+          if (kFull || sub + LPR * q < nch) raw[u][q] = __ldg(reinterpret_cast<const uint4*>(x + LPR * q * VEC));
+        }
+      }
+      row += step_r;
+      tk += step_t;
+      if (p.tpc > 1 && row >= heads) { row -= heads; ++tk; }
+    }
+  };
+  // a node's rows are asked for before its place in the tree is known
+  if constexpr (kTree) load_turn(0);
+
   if constexpr (kTree) {
     const int b = tok0 / p.n, i = tok0 - b * p.n;
     const int t = tree_node(p.plan.parents, p.plan.pos, b, p.n, i, &node_s);
@@ -197,9 +247,9 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
         }
         count = nwin;
         if (L.list_drafts && threadIdx.x == 0) {
-          for (int q = p0; q <= t; ++q)
-            if ((q + 1) % L.m == 0 && (q + 1) / L.m - 1 < L.N)
-              list[count++] = (ROW_DRAFT << kRowShift) | (b * L.T + node_s.at(q));
+          const int end = tree_entries_end(t, L.m, L.N);
+          for (int64_t q = tree_first_end(p0, L.m); q <= end; q += L.m)
+            list[count++] = (ROW_DRAFT << kRowShift) | (b * L.T + node_s.at((int)q));
         }
       }
       if (threadIdx.x == 0) L.info[tok0] = make_int4(t, t < 0 ? 0 : min(L.N, p0 / L.m), count, 0);
@@ -216,41 +266,8 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
   }
   __syncthreads();
 
-  // rows of this CTA: [row_begin, row_end) of one token, or all of tpc tokens
-  const int row_begin = blockIdx.y * p.rows_per_cta;
-  const int row_end = p.tpc > 1 ? heads : min(heads, row_begin + p.rows_per_cta);
-  const int n_rows = p.tpc > 1 ? p.tpc * heads : row_end - row_begin;
-  const int nch = p.d / VEC;
-  int tk = 0, row = row_begin + slot;                 // this lane group's next row
-  if (p.tpc > 1) { tk = slot / heads; row = slot - tk * heads; }
-  const int step_t = p.tpc > 1 ? RPC / heads : 0, step_r = RPC - step_t * heads;
-  bool have_cs = false;
-  int which = -1;
-  uint64_t gain[NCH][V2];
   for (int r0 = 0; r0 < n_rows; r0 += U * RPC) {
-    uint4 raw[U][NCH];
-    T* out[U];
-    int ut[U];                                        // token of the row (-1: nothing to do)
-    bool uk[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = r0 + u * RPC + slot < n_rows && pos_s[tk] >= 0;
-      const int k = row >= p.heads[0];
-      ut[u] = in ? tk : -1;
-      uk[u] = k;
-      if (in) {
-        const int h = row - k * p.heads[0];
-        const T* x = static_cast<const T*>(p.x[k]) + (off_s[k][tk] + h * p.xs[k][2] + sub * VEC);
-        out[u] = static_cast<T*>(p.y[k]) + (off_s[2 + k][tk] + h * p.d + sub * VEC);
-#pragma unroll
-        for (int q = 0; q < NCH; ++q) {
-          if (kFull || sub + LPR * q < nch) raw[u][q] = __ldg(reinterpret_cast<const uint4*>(x + LPR * q * VEC));
-        }
-      }
-      row += step_r;
-      tk += step_t;
-      if (p.tpc > 1 && row >= heads) { row -= heads; ++tk; }
-    }
+    if (!kTree || r0 > 0) load_turn(r0);
     if (!have_cs) {
       // (uniform over the CTA: the first turn of every warp)
       for (int j = threadIdx.x; j < p.tpc * npair; j += blockDim.x) {

@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) {
     int nd = 0;
-    for (int q = node_s.pos0; q <= t; ++q)
-      if ((q + 1) % p.m == 0 && (q + 1) / p.m - 1 < p.N) dnode[nd++] = node_s.at(q);
+    const int end = tree_entries_end(t, p.m, p.N);
+    for (int64_t q = tree_first_end(node_s.pos0, p.m); q <= end; q += p.m) dnode[nd++] = node_s.at((int)q);
     nd_s = nd;
     valid_s = 0;
   }
