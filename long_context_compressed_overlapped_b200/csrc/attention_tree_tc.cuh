@@ -14,7 +14,12 @@
 // the query.  M = 64 for S^T costs 1,033 + 776 cycles of operand reads a tile
 // (3,620 per 128 keys, against 3,090 with tiles of 128 keys), but one tile of
 // 128 at a time left the pipe idle for the softmax and the load: 7,250 cycles
-// per 128 keys.
+// per 128 keys.  With all SMs at work a tile takes some 3,000 cycles: 64 KB a
+// tile and node is 5.9 TB/s out of L2, near the 7.3 to 7.7 TB/s that a bare
+// stream of boxes reaches, so the tiles' way out of L2 bounds HCA calls of many
+// nodes (64 nodes over 8,192 entries: 119 us for 0.56 GB; dealing the tiles out
+// evenly over all SMs instead of two items a node changed nothing).  A CTA
+// cannot keep two nodes: O^T of one is half of TMEM.
 //
 // A node's keys are two runs.  Tiles of 64 consecutive committed entries
 // (HCA) arrive by TMA, four 64-dim chunks a box (an SM completes about one TMA
