@@ -401,9 +401,13 @@ def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True,
                k_out)
 
 
-def _tree_compress(kind, streams, ring, pos, parents, bias_a, m, bias_b, gain, rms_norm, rope_dims, rope_base, eps, out,
-                   out_scale):
+def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, gain=None, rms_norm=True,
+                       rope_dims=0, rope_base=10000.0, eps=1e-6, out=None, out_scale=None):
+    """Build the TreeCompressArgs struct (and keep the tensors it points to
+    alive in the returned list).  Returns (args, out, keep)."""
     csa = kind == "csa"
+    if len(streams) != (4 if csa else 2):
+        raise ValueError("csa takes four streams (a, b, za, zb), hca two (a, za)")
     x = streams[0]
     dev, dt, keep = x.device, x.dtype, []
     code = _dt(x)
@@ -423,12 +427,17 @@ def _tree_compress(kind, streams, ring, pos, parents, bias_a, m, bias_b, gain, r
         bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
         out=_arg("out", out, dev, shape, odt),
         out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
-    N.check(N.lib().tree_compress(C.byref(a), _raw_stream(dev.index)), "tree_compress")
+    return a, out, keep
+
+
+def _tree_compress(args, kw):
+    a, out, keep = tree_compress_args(*args, **kw)
+    N.check(N.lib().tree_compress(C.byref(a), _raw_stream(out.device.index)), "tree_compress")
+    del keep
     return out
 
 
-def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, gain=None, rms_norm=True, rope_dims=0,
-                  rope_base=10000.0, eps=1e-6, out=None, out_scale=None, stream=None):
+def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, stream=None, **kw):
     """The compressed entries that the nodes of draft trees complete.
 
     streams: (a, b, za, zb) for "csa" or (a, za) for "hca", each [B, T, c], the
@@ -437,11 +446,11 @@ def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, 
     for a node that follows the last committed token, < -1 for no node).
     out [B, T, c]: row i is written iff node i's token ends a block, the others
     are left as they were (a new out starts at zero).  With out_scale
-    [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys."""
+    [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys.
+    bias_b, gain, rms_norm, rope_dims, rope_base, eps as in csa_compress."""
     if len(streams) != (4 if kind == "csa" else 2):
         raise ValueError("csa takes four streams (a, b, za, zb), hca two (a, za)")
-    return _on(stream, streams[0].device, _tree_compress, kind, streams, ring, pos, parents, bias_a, m, bias_b, gain,
-               rms_norm, rope_dims, rope_base, eps, out, out_scale)
+    return _on(stream, streams[0].device, _tree_compress, (kind, streams, ring, pos, parents, bias_a, m), kw)
 
 
 def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, rope_dims, draft=None, k=0, qI=None,

@@ -9,6 +9,9 @@ a profiler to capture.
     python -m long_context_compressed_overlapped_b200.profile_case compress --calls 4
     python -m long_context_compressed_overlapped_b200.profile_case prefill --calls 2
     python -m long_context_compressed_overlapped_b200.profile_case prefill_tail --calls 2
+    python -m long_context_compressed_overlapped_b200.profile_case tree_csa --calls 3
+    python -m long_context_compressed_overlapped_b200.profile_case tree_hca --calls 3
+    python -m long_context_compressed_overlapped_b200.profile_case norm_rope --calls 3
 
 ``csa``: one CSA decode layer through ``compressed_attn_decode`` (indexer with
 e4m3 keys, top-k select, attention, combine); ``hca``: one HCA decode layer
@@ -29,7 +32,11 @@ indexer over 4-query tiles, then the row top-k) and compressed_attn_prefill;
 about 3 GB on the device.  ``prefill_tail``: indexer_topk for the last 16,384
 queries of csa_prefill_128k (positions 114,688 .. 131,071 against the layer's
 32,768 indexer keys: the longest score rows, 28,673 .. 32,768 entries);
-about 2.3 GB on the device.  The process exits non-zero if a bounded device
+about 2.3 GB on the device.  ``tree_csa`` / ``tree_hca``: one decode_1m layer's
+verification step for trees of 16 drafted tokens a sequence (tree_compress,
+compressed_attn_tree; CSA with the indexer's selection of each node);
+``norm_rope``: qk_norm_rope of 4,096 tokens x 64 query heads and one key row of
+512 dims (545 MB).  The process exits non-zero if a bounded device
 wait gave up.
 """
 
@@ -45,13 +52,17 @@ from . import api, native, runtime, synth
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("case", choices=("csa", "hca", "csa_fp8kv", "hca_fp8kv", "indexer", "indexer_256k", "compress",
-                                        "prefill", "prefill_tail"))
+                                        "prefill", "prefill_tail", "tree_csa", "tree_hca", "norm_rope"))
     ap.add_argument("--calls", type=int, default=4)
     a = ap.parse_args(argv)
     if a.case == "prefill":
         return prefill_case(a.calls)
     if a.case == "prefill_tail":
         return prefill_tail_case(a.calls)
+    if a.case.startswith("tree_"):
+        return tree_case(a.case[5:], a.calls)
+    if a.case == "norm_rope":
+        return norm_rope_case(a.calls)
     wl = synth.WORKLOADS["decode_1m_fp8kv" if a.case.endswith("_fp8kv") else
                          "decode_256k" if a.case.endswith("_256k") else "decode_1m"]
     kind = "hca" if a.case.startswith("hca") else "csa"
@@ -108,6 +119,31 @@ def prefill_tail_case(calls: int, nq: int = 16384) -> int:
     torch.cuda.synchronize()
     err = api.device_error()
     print(f"profile_case prefill_tail ({nq} queries, {N} keys): {calls} calls, device error {err}")
+    return 1 if err else 0
+
+
+def tree_case(kind: str, calls: int, T: int = 16) -> int:
+    wl = synth.WORKLOADS["decode_1m"]
+    step = runtime.TreeStep(wl, synth.tree_inputs(wl, T, "cuda", layers=(kind,)), torch.cuda.current_stream())
+    for _ in range(calls):
+        step()
+    torch.cuda.synchronize()
+    err = api.device_error()
+    print(f"profile_case tree_{kind} ({T} nodes a sequence): {calls} calls, device error {err}")
+    return 1 if err else 0
+
+
+def norm_rope_case(calls: int, n: int = 4096) -> int:
+    wl = synth.WORKLOADS["csa_prefill_128k"]
+    D = synth.Draw(wl.seed + 200, "cuda")
+    q, k = D.normal("q", (1, n, wl.H, wl.d), 1.0, torch.bfloat16), D.normal("k", (1, n, 1, wl.d), 1.0, torch.bfloat16)
+    gain = 1.0 + D.normal("gain", (wl.d,), 0.1)
+    pos = torch.arange(n, device="cuda", dtype=torch.int32)[None]
+    for _ in range(calls):
+        api.qk_norm_rope(q, k, pos, rope_dims=wl.r, q_gain=gain, k_gain=gain)
+    torch.cuda.synchronize()
+    err = api.device_error()
+    print(f"profile_case norm_rope (n={n}): {calls} calls, device error {err}")
     return 1 if err else 0
 
 

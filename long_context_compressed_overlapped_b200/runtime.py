@@ -178,6 +178,83 @@ class DecodeGraph:
         self.graph.replay()
 
 
+class TreeStep:
+    """One verification step over every layer of `layers` (as made by
+    synth.tree_inputs) for trees of drafted tokens: per layer, the entries that
+    the nodes complete (tree_compress: KV rows and, CSA, indexer keys), then
+    compressed_attn_tree.  The caches are only read: commit() takes the accepted
+    tokens into them.  Argument structs and workspaces are built once (one
+    workspace for all layers, which follow one another on the stream), so a
+    call only enqueues the library's kernels on `stream`; it can be captured
+    into a CUDA graph after it has run once."""
+
+    def __init__(self, wl: synth.Workload, layers, stream: torch.cuda.Stream, keep_idx: bool = False):
+        self.lib = native.lib()
+        self.wl, self.layers, self.stream = wl, layers, stream
+        stream.wait_stream(torch.cuda.current_stream(stream.device))
+        self.calls, self.idx, nbytes = [], [], 1
+        with torch.cuda.stream(stream):
+            for L in layers:
+                B, T, H, d = L["tq"].shape
+                dev, csa = L["tq"].device, L["kind"] == "csa"
+                draft = torch.zeros(B, T, d, dtype=L["tq"].dtype, device=dev)
+                comp = [api.tree_compress_args(L["kind"], L["ts"], L["ring"], L["pos"], L["parents"], L["bias_a"], L["m"],
+                                               bias_b=L["bias_b"], gain=L["kv_gain"], rope_dims=wl.r, out=draft)]
+                kw, idx = {}, None
+                if csa:
+                    f8 = L["kI_scale"] is not None
+                    dk = torch.zeros(B, T, wl.dI, dtype=torch.uint8 if f8 else L["tq"].dtype, device=dev)
+                    dks = torch.zeros(B, T, wl.dI // 128, dtype=torch.float32, device=dev) if f8 else None
+                    comp.append(api.tree_compress_args("csa", L["tis"], L["iring"], L["pos"], L["parents"], L["ibias_a"],
+                                                       L["m"], bias_b=L["ibias_b"], rms_norm=False, out=dk, out_scale=dks))
+                    if keep_idx:
+                        idx = torch.empty(B, T, wl.k, dtype=torch.int32, device=dev)
+                    kw = dict(k=wl.k, qI=L["tqI"], wI=L["tw"], kI=L["kI"], kI_scale=L["kI_scale"], draft_kI=dk,
+                              draft_kI_scale=dks, idx_out=idx)
+                args, out, keep = api.tree_attn_args(L["kind"], L["tq"], L["pos"], L["parents"], L["kv"], L["win"],
+                                                     L["tkv_raw"], L["sinks"], m=L["m"], rope_dims=wl.r, draft=draft,
+                                                     q_gain=L["q_gain"], kv_gain=L["kv_gain"], **kw)
+                nbytes = max(nbytes, self.lib.csahca_tree_workspace_size(C.byref(args)))
+                self.calls.append((comp, args, out, keep))
+                self.idx.append(idx)
+            self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=stream.device)
+        for _, args, _, _ in self.calls:
+            args.workspace, args.workspace_bytes = self.workspace.data_ptr(), nbytes
+        self.outputs = [c[2] for c in self.calls]
+
+    def __call__(self):
+        s = self.stream.cuda_stream
+        for comp, args, _, _ in self.calls:
+            for c, _, _ in comp:
+                native.check(self.lib.tree_compress(C.byref(c), s), "tree_compress")
+            native.check(self.lib.compressed_attn_tree(C.byref(args), s), "compressed_attn_tree")
+
+    def commit(self, paths: torch.Tensor) -> None:
+        """Take the accepted tokens into every layer's compressors, caches and
+        window: paths [B, n] holds each sequence's accepted nodes from the first
+        drafted token down, -1 behind the last.  One decode_compress a depth and
+        layer; L["pos"] moves on by the accepted tokens."""
+        with torch.cuda.stream(self.stream):
+            paths = paths.to(self.stream.device, torch.int64)
+            for L in self.layers:
+                csa = L["kind"] == "csa"
+                for j in range(paths.shape[1]):
+                    node = paths[:, j]
+                    pos = torch.where(node >= 0, L["pos"] + j, torch.full_like(L["pos"], -1))
+
+                    def take(x):
+                        return x[torch.arange(x.shape[0], device=x.device), node.clamp(min=0)].contiguous()
+                    kw = {}
+                    if csa:
+                        kw = dict(istreams=tuple(take(x) for x in L["tis"]), ibias_a=L["ibias_a"], ibias_b=L["ibias_b"],
+                                  iring=L["iring"], kI=L["kI"], kI_scale=L["kI_scale"])
+                    api.decode_compress(L["kind"], pos, tuple(take(x) for x in L["ts"]), L["ring"], L["kv"], m=L["m"],
+                                        bias_a=L["bias_a"], bias_b=L["bias_b"], kv_raw=take(L["tkv_raw"]), win=L["win"],
+                                        kv_gain=L["kv_gain"], rope_dims=self.wl.r, stream=self.stream, **kw)
+            for L in self.layers:
+                L["pos"] += (paths >= 0).sum(1).to(L["pos"].dtype)
+
+
 class HostIOGraph:
     """A decode step fed from host memory, captured as one CUDA graph with the
     host copies pipelined: on a copy stream the first layer's compressor

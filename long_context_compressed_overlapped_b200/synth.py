@@ -287,3 +287,42 @@ def decode_inputs(wl: Workload, device="cpu", ctx: int | None = None, B: int | N
             L["ibias_b"] = D.normal(f"{t}/ibias_b", (m, wl.dI), 0.1, torch.float32)
         out.append(L)
     return out
+
+
+def draft_tree(B: int, T: int, seed: int = 0, width: int = 6):
+    """parents [B][T] of random draft trees: node 0 follows the last committed
+    token, a later node one of the `width` nodes before it (or, rarely, the last
+    committed token itself)."""
+    g = torch.Generator().manual_seed(1000003 * int(seed) + T)
+    back = torch.randint(1, width + 1, (B, T), generator=g).tolist()
+    return [[max(-1, i - back[b][i]) if i else -1 for i in range(T)] for b in range(B)]
+
+
+def tree_inputs(wl: Workload, T: int, device="cpu", ctx: int | None = None, B: int | None = None, layers=None,
+                room: int = 0):
+    """decode_inputs of the same layers (caches with room for every entry that T
+    drafted tokens complete), and per layer the inputs of T drafted tokens a
+    sequence, the first at position ctx: tq [B, T, H, d], tkv_raw [B, T, d], the
+    compressors' streams ts (a, b, za, zb or a, za) [B, T, d]; CSA also tqI
+    [B, T, H_I, d_I], tw [B, T, H_I] and the indexer streams tis [B, T, d_I].
+    parents [B, T] int32 is the same tree in every layer."""
+    D = Draw(wl.seed + 7, device)
+    ctx = wl.ctx if ctx is None else ctx
+    B = wl.B if B is None else B
+    dt = wl.torch_dtype
+    sd = (1.0 / math.sqrt(wl.d)) if wl.dtype == "f32" else 1.0
+    out = decode_inputs(wl, device, ctx=ctx, B=B, layers=layers, room=room + T)
+    parents = torch.tensor(draft_tree(B, T, wl.seed), dtype=torch.int32, device=device)
+    for li, L in enumerate(out):
+        t = f"T{li}"
+        csa = L["kind"] == "csa"
+        L["parents"] = parents
+        L["tq"] = D.normal(f"{t}/q", (B, T, wl.H, wl.d), 1.0, dt)
+        L["tkv_raw"] = D.normal(f"{t}/kv_raw", (B, T, wl.d), sd, dt)
+        L["ts"] = tuple(D.normal(f"{t}/s{j}", (B, T, wl.d), sd, dt) for j in range(4 if csa else 2))
+        if csa:
+            sdi = (1.0 / math.sqrt(wl.dI)) if wl.dtype == "f32" else 1.0
+            L["tqI"] = D.normal(f"{t}/qI", (B, T, wl.HI, wl.dI), 1.0, dt)
+            L["tw"] = D.normal(f"{t}/w", (B, T, wl.HI), 1.0 / math.sqrt(wl.HI), torch.float32)
+            L["tis"] = tuple(D.normal(f"{t}/i{j}", (B, T, wl.dI), sdi, dt) for j in range(4))
+    return out

@@ -6,7 +6,7 @@ import ctypes as C
 import pytest
 import torch
 
-from long_context_compressed_overlapped_b200 import api, build, native as N
+from long_context_compressed_overlapped_b200 import api, build, native as N, synth
 from tests import tree_reference as R
 
 
@@ -162,3 +162,11 @@ def test_reference_paths():
                 path = R.path_of(row, i)
                 assert (path is None) == (p == R.NONE or (p >= 0 and R.path_of(row, p) is None))
                 assert path is None or (path[-1] == i and len(path) == R.node_position(row, 10, i) - 9)
+
+
+def test_tree_inputs_are_seeded():
+    wl = synth.WORKLOADS["decode_256k"]
+    a = synth.tree_inputs(wl, 5, "cpu", ctx=300, B=1)
+    b = synth.tree_inputs(wl, 5, "cpu", ctx=300, B=1)
+    assert torch.equal(a[0]["tq"], b[0]["tq"]) and torch.equal(a[1]["parents"], b[0]["parents"])
+    assert a[0]["parents"].lt(torch.arange(5)).all()
