@@ -318,7 +318,7 @@ def _arg(name, t, dev, shape, dtype, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
         return t.data_ptr()
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
@@ -369,8 +369,8 @@ def _norm_rope(q, k, pos, rope_dims, q_gain, k_gain, q_norm, k_norm, rope_base, 
     x = q if q is not None else k
     dev, dt, keep = x.device, x.dtype, []
     B, n, _, d = x.shape
-    a = N.NormRopeArgs(dtype=_dt(x), B=B, n=n, d=d, rope_dims=rope_dims, rope_base=rope_base, eps=eps, q_norm=bool(q_norm),
-                       k_norm=bool(k_norm), pos=_ints("pos", pos, dev, (B, n), keep))
+    a = N.NormRopeArgs(_dt(x), B, n, 0, 0, d, rope_dims, rope_base, eps, bool(q_norm), bool(k_norm))
+    a.pos = _ints("pos", pos, dev, (B, n), keep)
     if q is not None:
         a.HQ, st, a.q, a.q_out, a.q_gain, q_out = _heads("q", q, q_out, q_gain, dev, dt, B, n, d, keep)
         if st is not None:
@@ -462,26 +462,29 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     csa = kind == "csa"
     dev, dt, keep = q.device, q.dtype, []
     code = _dt(q)
-    B, T, H, d = q.shape
+    shape = q.shape
+    B, T, H, d = shape
     Nc = kv_cache.shape[1]
     w = win.shape[1] if win is not None else 0
     if out is None:
-        out = torch.zeros(q.shape, dtype=dt, device=dev)
-    a = N.TreeAttnArgs(kind=N.CSA if csa else N.HCA, dtype=code, B=B, T=T, H=H, d=d, N_cap=Nc, m=m, w=w,
-                       rope_dims=rope_dims, rope_base=rope_base, eps=eps, scale=scale, q_norm=bool(q_norm),
-                       kv_norm=bool(kv_norm), q=_arg("q", q, dev, q.shape, dt),
-                       pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
-                       q_gain=_floats("q_gain", q_gain, dev, (d,), keep),
-                       kv_gain=_floats("kv_gain", kv_gain, dev, (d,), keep),
-                       kv_cache=_arg("kv_cache", kv_cache, dev, (B, Nc, d), dt) if Nc else None,
-                       draft=_arg("draft", draft, dev, (B, T, d), dt, True),
-                       sinks=_floats("sinks", sinks, dev, (H,), keep, False), out=_arg("out", out, dev, q.shape, dt))
-    if w:
-        a.win = _arg("win", win, dev, (B, w, d), dt)
-        a.kv_raw = _arg("kv_raw", kv_raw, dev, (B, T, d), dt)
+        out = torch.zeros(shape, dtype=dt, device=dev)
+    row = (B, T, d)
+    # (in the struct's order)
+    a = N.TreeAttnArgs(
+        N.CSA if csa else N.HCA, code, B, T, H, d, Nc, m, w, k, rope_dims, rope_base, eps, scale, bool(q_norm),
+        bool(kv_norm), 0, 0, 0, 0,
+        _arg("q", q, dev, shape, dt), _ints("pos", pos, dev, (B,), keep), _ints("parents", parents, dev, (B, T), keep),
+        None if q_gain is None else _floats("q_gain", q_gain, dev, (d,), keep),
+        None if kv_gain is None else _floats("kv_gain", kv_gain, dev, (d,), keep),
+        _arg("kv_cache", kv_cache, dev, (B, Nc, d), dt) if Nc else None,
+        _arg("win", win, dev, (B, w, d), dt) if w else None,
+        _arg("kv_raw", kv_raw, dev, row, dt) if w else None,
+        None if draft is None else _arg("draft", draft, dev, row, dt),
+        _floats("sinks", sinks, dev, (H,), keep, False))
+    a.out = _arg("out", out, dev, shape, dt)
     if csa:
         if idx_in is not None:
-            k = idx_in.shape[2]
+            a.k = k = idx_in.shape[2]
             a.idx_in = _arg("idx_in", idx_in, dev, (B, T, k), torch.int32)
         else:
             if qI is None or wI is None or kI is None:
@@ -494,8 +497,8 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
             a.kI_scale = _floats("kI_scale", kI_scale, dev, (B, Nc, dI // 128), keep)
             a.draft_kI = _arg("draft_kI", draft_kI, dev, (B, T, dI), kI.dtype, True)
             a.draft_kI_scale = _floats("draft_kI_scale", draft_kI_scale, dev, (B, T, dI // 128), keep)
-        a.k = k
-        a.idx_out = _arg("idx_out", idx_out, dev, (B, T, k), torch.int32, True)
+        if idx_out is not None:
+            a.idx_out = _arg("idx_out", idx_out, dev, (B, T, k), torch.int32)
     return a, out, keep
 
 
@@ -503,12 +506,17 @@ def _attn_tree(args, kw, workspace):
     a, out, keep = tree_attn_args(*args, **kw)
     dev = out.device
     L = N.lib()
-    nbytes = L.csahca_tree_workspace_size(C.byref(a))
-    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    a.workspace = _arg("workspace", workspace, dev, workspace.shape, workspace.dtype)
-    a.workspace_bytes = workspace.numel() * workspace.element_size()
-    N.check(L.compressed_attn_tree(C.byref(a), _raw_stream(dev.index)), "compressed_attn_tree")
+    ref = C.byref(a)
+    nbytes = L.csahca_tree_workspace_size(ref)
+    if workspace is not None and workspace.numel() * workspace.element_size() >= nbytes:
+        a.workspace = _arg("workspace", workspace, dev, workspace.shape, workspace.dtype)
+    else:
+        workspace = torch.empty(nbytes + 1, dtype=torch.uint8, device=dev)
+        a.workspace = workspace.data_ptr()
+    a.workspace_bytes = nbytes
+    st = L.compressed_attn_tree(ref, _raw_stream(dev.index))
+    if st:
+        N.check(st, "compressed_attn_tree")
     del keep
     return out
 
