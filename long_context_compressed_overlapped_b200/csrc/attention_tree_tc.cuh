@@ -68,9 +68,16 @@ struct TreeSmem {
 static_assert(256 * kAttnRegsSoftmax + 32 * kTreeProducers * kAttnRegsProducer + 128 * kAttnRegsMma <= 72 * kTreeThreads,
               "the register split fits a 72-register launch");
 
-// Partial of one (node, split): m[H], l[H], O / l [D][H], fp32.
+// Partial of one (node, split), fp32: m[H], l[H], then O / l as [2 head groups][D]
+// rows of 32 heads, 128 bytes each, whose 16-byte piece j holds heads
+// 4 (j ^ (dim & 7)) .. + 3: as the threads write them into shared memory without
+// conflicts, so that a bulk copy takes 16 KB of it at once (stored from the
+// registers, 16 bytes a lane and 256 bytes apart, a partial took 10,600 cycles).
 constexpr int kTreePartialFloats = 2 * kAttnH + kAttnD * kAttnH;
 constexpr int kTreePartialBytes = kTreePartialFloats * 4;
+__host__ __device__ __forceinline__ int tree_partial_at(int dim, int head) {   // head % 4 == 0
+  return 2 * kAttnH + ((head >> 5) * kAttnD + dim) * 32 + ((((head & 31) >> 2) ^ (dim & 7)) << 2);
+}
 
 struct TreeAttnParams {
   const __nv_bfloat16* kv;               // [B * N, D]
@@ -177,6 +184,13 @@ __device__ __forceinline__ void tmem_ld16x256_x4(uint32_t taddr, float (&v)[16])
       : "r"(taddr));
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Every committed bulk group of this thread has completed, its writes made.
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Contiguous shared -> global copy (bulk-group completion).
+__device__ __forceinline__ void bulk_store(void* dst_gmem, const void* src_smem, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst_gmem), "r"(smem_u32(src_smem)),
+               "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
@@ -590,20 +604,40 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
           }
           group_sync(gid);
           if (!empty) {
+            // staged as the partial's rows: all four M-tiles in the key buffers
+            // where this is the CTA's last item (its last P.V has completed and
+            // no further keys come), else 64 dims at a time in P^T's buffers
             const float4* f4 = reinterpret_cast<const float4*>(stat_a + h0);
+            const bool last = id + (int)gridDim.x >= p.n_items;
 #pragma unroll 1
             for (int mt = 0; mt < kAttnMT; ++mt) {
               float o[32];
               tmem_ld32(tO + lane_base + mt * kAttnH + h0, o);
               tmem_wait_ld();
-              // this thread's dim, the group's 32 heads: 128 contiguous bytes
-              float4* dst = reinterpret_cast<float4*>(blk + 2 * kAttnH + (mt * 128 + tid) * kAttnH + h0);
+              float* dst = blk + 2 * kAttnH + (g * kAttnD + mt * 128) * 32;
+#pragma unroll 1
+              for (int half = 0; half < (last ? 1 : 2); ++half) {
+                uint8_t* stg = last ? sK + (g * kAttnMT + mt) * 16384 : sP + g * TreeSmem::P_BYTES;
+                const int row = last ? tid : tid & 63;
+                if (last || half == tid >> 6) {
 #pragma unroll
-              for (int e4 = 0; e4 < 8; ++e4) {
-                const float4 fc = f4[e4];
-                dst[e4] = make_float4(o[4 * e4] * fc.x, o[4 * e4 + 1] * fc.y, o[4 * e4 + 2] * fc.z, o[4 * e4 + 3] * fc.w);
+                  for (int e4 = 0; e4 < 8; ++e4) {
+                    const float4 fc = f4[e4];
+                    *reinterpret_cast<float4*>(stg + sw128_offset(row, 16 * e4)) =
+                        make_float4(o[4 * e4] * fc.x, o[4 * e4 + 1] * fc.y, o[4 * e4 + 2] * fc.z, o[4 * e4 + 3] * fc.w);
+                  }
+                }
+                fence_proxy_async_smem();
+                group_sync(gid);
+                if (tid == 0) {
+                  bulk_store(dst + half * 64 * 32, stg, last ? 16384 : 8192);
+                  bulk_commit();
+                  if (!last) bulk_wait_read<0>();
+                }
+                if (!last) group_sync(gid);
               }
             }
+            if (tid == 0) bulk_wait_all();             // written before the CTA may exit
           }
         } else {
           // o = O / (l + e^{z - m}), rope dims rotated back by -t.  A thread
@@ -690,7 +724,8 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
   const int tid = threadIdx.x;
   const float* P = reinterpret_cast<const float*>(p.partial) + (int64_t)node * p.splits * kTreePartialFloats;
   const int dp = tid >> 4, h4 = (tid & 15) * 4;          // dims d0 + 2 dp, + 1; heads h4 .. h4 + 3
-  const float* src = P + 2 * kAttnH + (d0 + 2 * dp) * kAttnH + h4;
+  const float* src0 = P + tree_partial_at(d0 + 2 * dp, h4);
+  const float* src1 = P + tree_partial_at(d0 + 2 * dp + 1, h4);
   // the position, the headers and the first splits' O are asked for together
   // (the partial blocks of a place without a node hold no numbers, but exist)
   const int t = p.node_pos[node];
@@ -700,8 +735,8 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     if (u < p.splits) {
-      x[u] = *reinterpret_cast<const float4*>(src + (int64_t)u * kTreePartialFloats);
-      y[u] = *reinterpret_cast<const float4*>(src + (int64_t)u * kTreePartialFloats + kAttnH);
+      x[u] = *reinterpret_cast<const float4*>(src0 + (int64_t)u * kTreePartialFloats);
+      y[u] = *reinterpret_cast<const float4*>(src1 + (int64_t)u * kTreePartialFloats);
     }
   }
   // weights: thread (head h, part) takes the splits part, part + 4, ...
@@ -743,8 +778,8 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (s0 + u < p.splits) {
-          x[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats);
-          y[u] = *reinterpret_cast<const float4*>(src + (int64_t)(s0 + u) * kTreePartialFloats + kAttnH);
+          x[u] = *reinterpret_cast<const float4*>(src0 + (int64_t)(s0 + u) * kTreePartialFloats);
+          y[u] = *reinterpret_cast<const float4*>(src1 + (int64_t)(s0 + u) * kTreePartialFloats);
         }
       }
     }
