@@ -88,6 +88,7 @@ struct TreeAttnParams {
   const float* sinks;
   int list_stride;                       // w + T
   int k, N, T;
+  int idx_given;                         // idx is the caller's, not an earlier kernel's
   int n_items, splits;
   float scale_log2;
   int rope_dims;
@@ -100,6 +101,11 @@ struct TreeItem { int node, split, t, full, tail, nlist, tile0, tile1; };
 __device__ __forceinline__ int4 tree_info(const TreeAttnParams& p, int id) {
   return id < p.n_items ? __ldg(p.info + id / p.splits) : make_int4(-1, 0, 0, 0);
 }
+// First tile of a split: the first total % splits of them take one more.
+__device__ __forceinline__ int tree_tile0(int total, int split, int splits) {
+  const int q = total / splits;
+  return q * split + min(split, total - q * splits);
+}
 __device__ __forceinline__ TreeItem tree_item(const TreeAttnParams& p, int id, const int4& f) {
   TreeItem it;
   it.node = id / p.splits;
@@ -109,8 +115,8 @@ __device__ __forceinline__ TreeItem tree_item(const TreeAttnParams& p, int id, c
   it.tail = p.idx ? p.k : f.y % kTreeTile;
   it.nlist = it.tail + f.z;
   const int total = f.x < 0 ? 0 : it.full + (it.nlist + kTreeTile - 1) / kTreeTile;
-  it.tile0 = (int)((int64_t)total * it.split / p.splits);
-  it.tile1 = (int)((int64_t)total * (it.split + 1) / p.splits);
+  it.tile0 = tree_tile0(total, it.split, p.splits);
+  it.tile1 = tree_tile0(total, it.split + 1, p.splits);
   return it;
 }
 // Entry j of the node's list as it stands in memory (the selection's index or
@@ -239,7 +245,16 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
   const uint32_t tS = tmem;                              // S^T of buffer b: columns [64 b, ...), M = 64: keys 16 q ..
                                                          // 16 q + 15 in lanes 32 q .. 32 q + 15
   const uint32_t tO = tmem + 128;                        // O^T M-tile j: columns [128 + j H, ...)
-  // the plan, the finished rows and the selection come from earlier kernels
+  // the plan, the finished rows and the selection come from earlier kernels; a
+  // selection that the caller gave is an input, and the rows that it names for
+  // the first tile (as it would be for a whole window) go to L2 meanwhile
+  if (p.idx_given && warp >= 8 && warp < kWarpS) {
+    const int node = blockIdx.x / p.splits;
+    const int tiles = (p.k + p.list_stride - p.T + kTreeTile - 1) / kTreeTile;
+    const int j = tree_tile0(tiles, blockIdx.x - node * p.splits, p.splits) * kTreeTile + 4 * (warp - 8) + (lane >> 3);
+    const int e = j < p.k ? __ldg(p.idx + (int64_t)node * p.k + j) : -1;
+    if (e >= 0 && e < p.N) prefetch_l2_line(p.kv + ((int64_t)(node / p.T) * p.N + e) * kAttnD + (lane & 7) * 64);
+  }
   griddep_wait();
   griddep_launch_dependents();
 

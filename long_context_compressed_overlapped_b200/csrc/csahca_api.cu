@@ -1579,7 +1579,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   p.rows[ROW_RING] = static_cast<const __nv_bfloat16*>(a->win);
   p.rows[ROW_TREE] = reinterpret_cast<const __nv_bfloat16*>(ws + L.rows);
   p.rows[ROW_DRAFT] = static_cast<const __nv_bfloat16*>(a->draft);
-  p.idx = sel; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
+  p.idx = sel; p.idx_given = sel && sel == a->idx_in; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
   p.turn = reinterpret_cast<const float2*>(ws + L.turn);
   p.sinks = a->sinks; p.list_stride = a->w + a->T; p.k = a->k; p.N = a->N_cap; p.T = a->T;
   p.splits = L.splits; p.n_items = nodes * L.splits; p.scale_log2 = scale * kLog2e; p.rope_dims = a->rope_dims;
