@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (r0 + u * RPC >= n_rows) break;              // (uniform over the CTA)
+      const bool in = ut[u] >= 0;
+      if (LPR == 32 && !in) continue;                 // (the warp's one row)
       const int k = uk[u];
       if (k != which) {
         which = k;
@@ -301,11 +303,10 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
           }
         }
       }
-      const bool in = ut[u] >= 0;
       uint64_t v[NCH][V2], s2 = 0;
 #pragma unroll
       for (int q = 0; q < NCH; ++q) {
-        if (in && (kFull || sub + LPR * q < nch)) {
+        if ((LPR == 32 || in) && (kFull || sub + LPR * q < nch)) {
           f2_load<T>(raw[u][q], v[q]);
 #pragma unroll
           for (int e = 0; e < V2; ++e) s2 = f2_fma(v[q][e], v[q][e], s2);
@@ -320,15 +321,22 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
 #pragma unroll
       for (int q = 0; q < NCH; ++q) {
         const int ch = sub + LPR * q;
-        if (in && (kFull || ch < nch)) {
+        if ((LPR == 32 || in) && (kFull || ch < nch)) {
 #pragma unroll
-          for (int e = 0; e < V2; ++e) v[q][e] = f2_mul(v[q][e], f2_mul(gain[q][e], inv2));
+          for (int e = 0; e < V2; ++e) v[q][e] = f2_mul(f2_mul(v[q][e], gain[q][e]), inv2);
           const int j0 = (ch * VEC - (p.d - p.rope_dims)) >> 1;
-          if (j0 + V2 > 0) {
+          const float2* cs = cs_s + ut[u] * npair + j0;
+          if (j0 >= 0) {
+#pragma unroll
+            for (int e = 0; e < V2; ++e) {
+              const float2 c = cs[e], x = f2_unpack(v[q][e]);
+              v[q][e] = f2_pack(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
+            }
+          } else if (j0 + V2 > 0) {                   // the rope dims begin inside the piece
 #pragma unroll
             for (int e = 0; e < V2; ++e) {
               if (j0 + e >= 0) {
-                const float2 c = cs_s[ut[u] * npair + j0 + e], x = f2_unpack(v[q][e]);
+                const float2 c = cs[e], x = f2_unpack(v[q][e]);
                 v[q][e] = f2_pack(x.x * c.x - x.y * c.y, x.x * c.y + x.y * c.x);
               }
             }
