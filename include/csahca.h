@@ -491,7 +491,7 @@ int cp_attn_merge(const csahca_cp_merge_args* args, void* stream);
  * Layout: q [B, n, HQ, d], k [B, n, HK, d] with the dims of a head contiguous
  *   and the batch, token and head strides of q_stride / k_stride (in elements,
  *   multiples of 16 bytes, >= 0; all three 0: contiguous), so that heads may be
- *   slices of one projection; pos [B, n] int32 on the device; gains [d] f32;
+ *   slices of one projection or broadcast along some of the three; pos [B, n] int32 on the device; gains [d] f32;
  *   q_out [B, n, HQ, d], k_out [B, n, HK, d] contiguous (either may be its own
  *   input where that is contiguous).  HQ or HK = 0: that side is left out.
  *   The rows of a token with pos < 0 (padding) are left as they were.

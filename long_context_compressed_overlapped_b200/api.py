@@ -357,6 +357,9 @@ def _heads(name, t, out, gain, dev, dt, B, n, d, keep):
         strides = t.stride()
         if d > 1 and strides[3] != 1:
             raise ValueError(f"{name}: the dims of a head must be contiguous")
+        if not any(strides[:3]):                 # one row for every head (the library's mark of contiguous rows)
+            t, strides = t.contiguous(), None
+            keep.append(t)
     if out is None:
         out = torch.empty_like(t, memory_format=torch.contiguous_format)
         o = out.data_ptr()

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
     if (tid == 0) {
       float s = 0.f;
       for (int k = 0; k < kTsThreads / 32; ++k) s += part_s[k];
-      dscore[x] = s;
+      dscore[x] = s == s ? s : -INFINITY;            // (NaN: last, so that the ranks stay distinct)
     }
     __syncthreads();
   }

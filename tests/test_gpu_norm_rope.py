@@ -101,6 +101,16 @@ def test_strided_slices_of_one_projection_and_in_place(dt):
         api.qk_norm_rope(wide.transpose(2, 3), None, torch.zeros(2, 13, device=DEV, dtype=torch.int32), rope_dims=0)
 
 
+def test_broadcast_rows():
+    """Expanded inputs: strides of 0 along any dims, all three among them."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    pos = torch.arange(6, device=DEV, dtype=torch.int32).view(2, 3) * 77
+    for x in (torch.randn(1, 1, 1, 64, generator=g, device=DEV), torch.randn(2, 1, 5, 64, generator=g, device=DEV),
+              torch.randn(1, 3, 1, 64, generator=g, device=DEV)):
+        y, _ = api.qk_norm_rope(x.expand(2, 3, 5, 64), None, pos, rope_dims=16)
+        check(y, reference(x.expand(2, 3, 5, 64), pos, 16, None, True), torch.float32, 64, np.ones((2, 3), bool))
+
+
 def test_zero_rows_and_large_rows():
     x = torch.zeros(1, 3, 2, 64, device=DEV)
     x[0, 1] = 1e15

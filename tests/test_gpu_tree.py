@@ -234,6 +234,46 @@ def test_attention_many_items(B, T, pos, kind):
     assert api.device_error() == 0
 
 
+@pytest.mark.parametrize("heads", [SMALL, HEADS16, dict(dt=torch.float32, H=5, d=512, r=512)], ids=["f32", "16h", "f32-512"])
+def test_attention_on_cuda_cores_in_splits(heads):
+    """Few nodes over many keys: the splits of the CUDA-core path and their join."""
+    for kind, pos, k in (("hca", [5000, 4700], 0), ("csa", [40000, 9], 4000)):
+        s = attn_case(kind, 2, 3, pos, "padded", 1 if kind == "hca" else 4, 16, k, seed=8, **heads)
+        out = run_attn(s, out=torch.full_like(s["q"], 7.0))
+        check_attn(s, out)
+    assert api.device_error() == 0
+
+
+@pytest.mark.parametrize("heads", [SMALL, TC], ids=["f32", "tc"])
+def test_entries_past_the_capacity_are_no_keys(heads):
+    """A full cache: what the path completes beyond N_cap is not stored by a
+    decode step, so no node sees it, and the indexer does not offer it."""
+    s = attn_case("hca", 1, 9, [60], "chain", 4, 16, N=16, seed=5, **heads)             # entries 15 | 16, 17 are past it
+    out = run_attn(s)
+    check_attn(s, out)
+    s = attn_case("csa", 1, 9, [60], "chain", 4, 16, 20, N=16, seed=5, **heads)
+    g, dt = gen(3), heads["dt"]
+    qI, wI = whole(g, 1, 3, dt, 1, 9, 2, 32), whole(g, 1, 4, torch.float32, 1, 9, 2)
+    kI, dk = whole(g, 0, 3, dt, 1, 16, 32), whole(g, 4, 5, dt, 1, 9, 32)
+    idx = torch.empty(1, 9, 20, dtype=torch.int32, device=DEV)
+    run_attn(s, k=20, qI=qI, wI=wI, kI=kI, draft_kI=dk, idx_out=idx)
+    got = npy(idx)[0]
+    assert (got[2] == list(range(15)) + [-1] * 5).all() and (got[8] == list(range(15)) + [16 + 3] + [-1] * 4).all()
+
+
+def test_nan_scores_stay_in_the_row():
+    """Drafted keys of NaN rank last; no row of the selection runs over."""
+    s = attn_case("csa", 1, 12, [2], "chain", 1, 0, 1, seed=1, **SMALL)
+    s["draft"].normal_()
+    qI, wI = torch.ones(1, 12, 2, 32, device=DEV), torch.ones(1, 12, 2, device=DEV)
+    kI, dk = torch.ones(1, s["N"], 32, device=DEV), torch.full((1, 12, 32), float("nan"), device=DEV)
+    idx = torch.full((1, 13, 3), -9, dtype=torch.int32, device=DEV)
+    run_attn(s, k=3, qI=qI, wI=wI, kI=kI, draft_kI=dk, idx_out=idx[:, :12])
+    assert (idx[0, 12] == -9).all() and (idx[0, :12, :2] == torch.tensor([0, 1], device=DEV)).all()
+    assert (idx[0, :12, 2] >= s["N"]).all()                                            # the one free place: a drafted entry
+    assert api.device_error() == 0
+
+
 @pytest.mark.parametrize("heads", [SMALL, TC], ids=["f32", "tc"])
 def test_without_drafted_entries_gains_or_norms(heads):
     for kind, k in (("hca", 0), ("csa", 30)):
