@@ -546,10 +546,13 @@ int qk_norm_rope(const csahca_norm_rope_args* args, void* stream);
  *   S = 2), slot p % R holding token p for the R tokens before pos[b]; bias_a,
  *   bias_b [m, c] f32; gain [c] f32 or NULL (ones); out [B, T, c] (dtype), or
  *   for out_dtype E4M3 codes with out_scale [B, T, c / 128] (decode_compress's
- *   rule for indexer keys).
+ *   rule for indexer keys), or for out_dtype E4M3 with kv_rows != 0 FP8 KV rows
+ *   [B, T, csahca_kv_row_bytes] (out_scale unused), as decode_compress stores
+ *   entries with kv_dtype E4M3.
  * Constraints: dtype F32 (c % 4 == 0, c <= 512) or BF16 (c % 8 == 0, c <=
  *   1024); R <= 512; rope_dims as in csa_compress and <= 512; out_dtype =
- *   dtype, or E4M3 with dtype BF16 and c % 128 == 0.  No workspace. */
+ *   dtype, or E4M3 with dtype BF16 and c % 128 == 0 (kv_rows: c and rope_dims as
+ *   csahca_kv_row_bytes takes them).  No workspace. */
 typedef struct {
   int32_t kind;
   int32_t dtype, out_dtype;
@@ -559,7 +562,7 @@ typedef struct {
   int32_t rope_dims;
   float rope_base;     /* 0 -> 10000 */
   float eps;           /* 0 -> 1e-6 */
-  int32_t reserved0;
+  int32_t kv_rows;     /* out_dtype E4M3: FP8 KV rows */
   const int32_t* pos;
   const int32_t* parents;
   const void* a;
@@ -600,8 +603,11 @@ int tree_compress(const csahca_tree_compress_args* args, void* stream);
  *   [B, T, d]; pos [B], parents [B, T]; gains [d] f32 or NULL (ones); sinks [H].
  *   out may not be q.  Cache, ring and draft rows that no node sees are not read
  *   into any result.  With no key at all, or an infinite sink, a row is 0.
+ * kv_dtype CSAHCA_E4M3: kv_cache and draft hold FP8 KV rows (layout above), read
+ *   as the rows they stand for; dtype BF16, H = 64, d = 512, rope_dims 64 or
+ *   128, else CSAHCA_ERR_UNSUPPORTED.  Any other kv_dtype: rows of `dtype`.
  * Constraints: d % 32 == 0, d <= 512; rope_dims even, <= d; k <= 4096 where
- *   draft_kI is given; caches of `dtype` rows (F32 or BF16).
+ *   draft_kI is given.
  * Workspace: csahca_tree_workspace_size(). */
 typedef struct {
   int32_t kind;
@@ -618,6 +624,8 @@ typedef struct {
   int32_t q_norm, kv_norm;
   int32_t HI, dI;
   int32_t qI_dtype, kI_dtype;
+  int32_t kv_dtype;    /* CSAHCA_E4M3: FP8 KV rows; else rows of dtype */
+  int32_t reserved0;
   const void* q;
   const int32_t* pos;
   const int32_t* parents;

@@ -405,7 +405,7 @@ def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True,
 
 
 def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=None, gain=None, rms_norm=True,
-                       rope_dims=0, rope_base=10000.0, eps=1e-6, out=None, out_scale=None):
+                       rope_dims=0, rope_base=10000.0, eps=1e-6, out=None, out_scale=None, kv_fp8=False):
     """Build the TreeCompressArgs struct (and keep the tensors it points to
     alive in the returned list).  Returns (args, out, keep)."""
     csa = kind == "csa"
@@ -415,20 +415,21 @@ def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=N
     dev, dt, keep = x.device, x.dtype, []
     code = _dt(x)
     B, T, c = shape = x.shape
-    f8 = out_scale is not None
+    f8 = kv_fp8 or out_scale is not None
     odt = torch.uint8 if f8 else dt
+    oshape = (B, T, N.lib().csahca_kv_row_bytes(N.E4M3, c, rope_dims)) if kv_fp8 else shape
     if out is None:
-        out = torch.zeros(B, T, c, dtype=odt, device=dev)
+        out = torch.zeros(oshape, dtype=odt, device=dev)
     p = [_arg("streams", t, dev, shape, dt) for t in streams]
     a = N.TreeCompressArgs(
         kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
-        rms_norm=bool(rms_norm), rope_dims=rope_dims, rope_base=rope_base, eps=eps,
+        rms_norm=bool(rms_norm), rope_dims=rope_dims, rope_base=rope_base, eps=eps, kv_rows=bool(kv_fp8),
         pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
         a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
         ring=_arg("ring", ring, dev, (B, 2 * m, 4, c) if csa else (B, m, 2, c), dt),
         bias_a=_floats("bias_a", bias_a, dev, (m, c), keep, False),
         bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
-        out=_arg("out", out, dev, shape, odt),
+        out=_arg("out", out, dev, oshape, odt),
         out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
     return a, out, keep
 
@@ -449,7 +450,8 @@ def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, stream=None, 
     for a node that follows the last committed token, < -1 for no node).
     out [B, T, c]: row i is written iff node i's token ends a block, the others
     are left as they were (a new out starts at zero).  With out_scale
-    [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys.
+    [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys; with
+    kv_fp8, FP8 KV rows (uint8 [B, T, csahca_kv_row_bytes]).
     bias_b, gain, rms_norm, rope_dims, rope_base, eps as in csa_compress."""
     if len(streams) != (4 if kind == "csa" else 2):
         raise ValueError("csa takes four streams (a, b, za, zb), hca two (a, za)")
@@ -472,17 +474,20 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     if out is None:
         out = torch.zeros(shape, dtype=dt, device=dev)
     row = (B, T, d)
+    # a uint8 cache holds FP8 KV rows, and so do the drafted entries
+    f8 = kv_cache.dtype is torch.uint8
+    cdt, cd = (torch.uint8, N.lib().csahca_kv_row_bytes(N.E4M3, d, rope_dims)) if f8 else (dt, d)
     # (in the struct's order)
     a = N.TreeAttnArgs(
         N.CSA if csa else N.HCA, code, B, T, H, d, Nc, m, w, k, rope_dims, rope_base, eps, scale, bool(q_norm),
-        bool(kv_norm), 0, 0, 0, 0,
+        bool(kv_norm), 0, 0, 0, 0, N.E4M3 if f8 else code, 0,
         _arg("q", q, dev, shape, dt), _ints("pos", pos, dev, (B,), keep), _ints("parents", parents, dev, (B, T), keep),
         None if q_gain is None else _floats("q_gain", q_gain, dev, (d,), keep),
         None if kv_gain is None else _floats("kv_gain", kv_gain, dev, (d,), keep),
-        _arg("kv_cache", kv_cache, dev, (B, Nc, d), dt) if Nc else None,
+        _arg("kv_cache", kv_cache, dev, (B, Nc, cd), cdt) if Nc else None,
         _arg("win", win, dev, (B, w, d), dt) if w else None,
         _arg("kv_raw", kv_raw, dev, row, dt) if w else None,
-        None if draft is None else _arg("draft", draft, dev, row, dt),
+        None if draft is None else _arg("draft", draft, dev, (B, T, cd), cdt),
         _floats("sinks", sinks, dev, (H,), keep, False))
     a.out = _arg("out", out, dev, shape, dt)
     if csa:
@@ -532,7 +537,8 @@ def compressed_attn_tree(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *,
     q [B, T, H, d] raw queries of the drafted tokens; pos [B] the first drafted
     token's position; parents [B, T] as in tree_compress; kv_cache [B, N_cap, d],
     win [B, w, d] (the committed tokens'); kv_raw [B, T, d] the drafted tokens'
-    raw window rows; draft [B, T, d] the entries they complete (tree_compress).
+    raw window rows; draft [B, T, d] the entries they complete (tree_compress);
+    uint8 kv_cache and draft: FP8 KV rows.
     CSA: idx_in [B, T, k] (N_cap + j names draft row j), or k with qI, wI, kI
     (kI_scale) and draft_kI (draft_kI_scale) for the lightning indexer; idx_out
     [B, T, k] receives the selection.  Rows of places without a node are left as

@@ -80,8 +80,10 @@ __host__ __device__ __forceinline__ int tree_partial_at(int dim, int head) {   /
 }
 
 struct TreeAttnParams {
-  const __nv_bfloat16* kv;               // [B * N, D]
-  const __nv_bfloat16* rows[3];          // ROW_RING, ROW_TREE, ROW_DRAFT bases
+  const uint8_t* kv;                     // cache rows [B * N]
+  const uint8_t* rows[3];                // ROW_RING, ROW_TREE (bf16 rows), ROW_DRAFT (as the cache's) bases
+  int row_bytes;                         // of a cache row: 2 D, or an FP8 KV row's
+  int nope_chunks;                       // FP8 KV rows: 64-dim chunks of codes, (D - rope_dims) / 64
   const int* idx;                        // CSA: [nodes, k]; null: HCA
   const int* list; const int4* info;
   const float2* turn;                    // [nodes][rope_dims / 2] cos, sin of the node's angles
@@ -106,13 +108,14 @@ __device__ __forceinline__ int tree_tile0(int total, int split, int splits) {
   const int q = total / splits;
   return q * split + min(split, total - q * splits);
 }
+template <bool kF8>
 __device__ __forceinline__ TreeItem tree_item(const TreeAttnParams& p, int id, const int4& f) {
   TreeItem it;
   it.node = id / p.splits;
   it.split = id - it.node * p.splits;
   it.t = f.x;
-  it.full = p.idx ? 0 : f.y / kTreeTile;
-  it.tail = p.idx ? p.k : f.y % kTreeTile;
+  it.full = kF8 || p.idx ? 0 : f.y / kTreeTile;        // (FP8 rows are widened on their way: all gathered)
+  it.tail = p.idx ? p.k : f.y - it.full * kTreeTile;
   it.nlist = it.tail + f.z;
   const int total = f.x < 0 ? 0 : it.full + (it.nlist + kTreeTile - 1) / kTreeTile;
   it.tile0 = tree_tile0(total, it.split, p.splits);
@@ -127,16 +130,20 @@ __device__ __forceinline__ int tree_entry(const TreeAttnParams& p, const TreeIte
   if (j >= it.tail) return __ldg(p.list + (int64_t)it.node * p.list_stride + (j - it.tail));
   return p.idx ? __ldg(p.idx + (int64_t)it.node * p.k + j) : it.full * kTreeTile + j;
 }
-__device__ __forceinline__ const __nv_bfloat16* tree_row(const TreeAttnParams& p, const TreeItem& it, int j, int e) {
+// (*cached: a row of the cache's or the drafted entries' kind)
+__device__ __forceinline__ const uint8_t* tree_row(const TreeAttnParams& p, const TreeItem& it, int j, int e, bool* cached) {
+  *cached = true;
   if (e < 0) return nullptr;
   if (j >= it.tail) {
     const int kind = e >> kRowShift;
-    const __nv_bfloat16* base = kind == ROW_RING ? p.rows[0] : kind == ROW_TREE ? p.rows[1] : p.rows[2];
-    return base + (int64_t)(e & kRowMask) * kAttnD;
+    const int64_t r = e & kRowMask;
+    *cached = kind == ROW_DRAFT;
+    return kind == ROW_RING ? p.rows[0] + r * (2 * kAttnD) : kind == ROW_TREE ? p.rows[1] + r * (2 * kAttnD)
+                                                                              : p.rows[2] + r * p.row_bytes;
   }
   const int b = it.node / p.T;
-  if (e < p.N) return p.kv + ((int64_t)b * p.N + e) * kAttnD;
-  if (e - p.N < p.T && p.rows[ROW_DRAFT]) return p.rows[ROW_DRAFT] + ((int64_t)b * p.T + (e - p.N)) * kAttnD;
+  if (e < p.N) return p.kv + ((int64_t)b * p.N + e) * p.row_bytes;
+  if (e - p.N < p.T && p.rows[ROW_DRAFT]) return p.rows[ROW_DRAFT] + ((int64_t)b * p.T + (e - p.N)) * p.row_bytes;
   raise_device_error(DEVERR_BAD_INDEX);
   return nullptr;
 }
@@ -200,6 +207,24 @@ __device__ __forceinline__ void bulk_store(void* dst_gmem, const void* src_smem,
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// 8 e4m3 codes times the block scale as 8 bf16.
+__device__ __forceinline__ uint4 f8x8_to_bf16(uint2 codes, float scale) {
+  const uint32_t c[2] = {codes.x, codes.y};
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((c[i >> 1] >> (16 * (i & 1))) & 0xffffu), __NV_E4M3)));
+    w[i] = pack_bf16x2(f.x * scale, f.y * scale);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// kF8: the cache and the drafted entries are FP8 KV rows.  Every tile is
+// gathered, and the producers widen the codes to bf16 between the load and the
+// shared-memory row (through registers, half a tile at a time), as a row stands
+// for decode(code) * scale; ring and tree rows are bf16 and are copied.
+template <bool kF8>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_constant__ CUtensorMap q_rows,
                     const __grid_constant__ TreeAttnParams p) {
@@ -253,7 +278,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     const int tiles = (p.k + p.list_stride - p.T + kTreeTile - 1) / kTreeTile;
     const int j = tree_tile0(tiles, blockIdx.x - node * p.splits, p.splits) * kTreeTile + 4 * (warp - 8) + (lane >> 3);
     const int e = j < p.k ? __ldg(p.idx + (int64_t)node * p.k + j) : -1;
-    if (e >= 0 && e < p.N) prefetch_l2_line(p.kv + ((int64_t)(node / p.T) * p.N + e) * kAttnD + (lane & 7) * 64);
+    if (e >= 0 && e < p.N) prefetch_l2_line(p.kv + ((int64_t)(node / p.T) * p.N + e) * p.row_bytes + min((lane & 7) * 128, p.row_bytes - 16));
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -271,7 +296,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     bool stop = false;                                   // warp-uniform
     int4 f = tree_info(p, blockIdx.x);
     for (int id = blockIdx.x; id < p.n_items && !stop; id += gridDim.x) {
-      const TreeItem it = tree_item(p, id, f);
+      const TreeItem it = tree_item<kF8>(p, id, f);
       f = tree_info(p, id + gridDim.x);
       if (it.tile1 <= it.tile0) continue;
       if (pw == 0) {
@@ -296,12 +321,60 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         const bool box = tile < it.full;
         const int off = (tile - it.full) * kTreeTile;
         const int fill = box ? 0 : (it.nlist - off + 15) & ~15;   // rows that the P.V MMAs read
-        const __nv_bfloat16* src = nullptr;
+        const uint8_t* src = nullptr;
+        bool cached = true;
         if (!box) {
-          src = tree_row(p, it, off + row, e);
+          src = tree_row(p, it, off + row, e, &cached);
           e = tree_entry(p, it, off + kTreeTile + row);
         }
         const bool live = src != nullptr;
+        if constexpr (kF8) {
+          const bool codes = cached;
+          for (int h = 0; h < 2; ++h) {
+            // this lane's 8 dims of the half's four chunks, asked for before the buffer is free
+            uint4 raw[kTreeHalfChunks];
+            float scale[kTreeHalfChunks];
+#pragma unroll
+            for (int c = 0; c < kTreeHalfChunks; ++c) {
+              const int cc = h * kTreeHalfChunks + c;
+              raw[c] = make_uint4(0u, 0u, 0u, 0u);
+              scale[c] = 0.f;
+              if (live) {
+                if (codes && cc < p.nope_chunks) {
+                  const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + cc * 64 + piece * 8));
+                  raw[c].x = v.x;
+                  raw[c].y = v.y;
+                  scale[c] = __ldg(reinterpret_cast<const float*>(src + kAttnD + p.rope_dims + 4 * cc));
+                } else {
+                  const int o = codes ? p.nope_chunks * 64 + (cc - p.nope_chunks) * 128 : cc * 128;
+                  raw[c] = __ldg(reinterpret_cast<const uint4*>(src + o + piece * 16));
+                }
+              }
+            }
+            int ok = 1;
+            if (lane == 0) ok = mbar_wait(&bar_pv[buf][h], ph ^ 1, &abort_flag);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) { stop = true; break; }
+            if (row < fill) {
+#pragma unroll
+              for (int c = 0; c < kTreeHalfChunks; ++c) {
+                const int cc = h * kTreeHalfChunks + c;
+                const uint4 w = live && codes && cc < p.nope_chunks
+                                    ? f8x8_to_bf16(make_uint2(raw[c].x, raw[c].y), scale[c]) : raw[c];
+                *reinterpret_cast<uint4*>(dst + cc * TreeSmem::K_CHUNK + sw128_offset(row, piece * 16)) = w;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_kfull[buf][h]);
+          }
+          if (!stop && tile + 1 < it.tile1) {
+            bool nc;
+            const uint8_t* nx = tree_row(p, it, off + kTreeTile + row, e, &nc);
+            if (nx && piece * 128 < (nc ? p.row_bytes : 2 * kAttnD)) prefetch_l2_line(nx + piece * 128);
+          }
+          continue;
+        }
         if (!live) src = p.kv;
         for (int h = 0; h < 2; ++h) {
           int ok = 1;
@@ -326,7 +399,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
               for (int c = 0; c < kTreeHalfChunks; ++c) {
                 const int cc = h * kTreeHalfChunks + c;
                 cp_async16_or_zero(dst + cc * TreeSmem::K_CHUNK + sw128_offset(row, piece * 16),
-                                   src + cc * 64 + piece * 8, live);
+                                   src + cc * 128 + piece * 16, live);
               }
             }
             cp_async_commit();
@@ -345,8 +418,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         if (lane == 0) mbar_arrive(&bar_kfull[buf][1]);
         if (tile + 1 < it.tile1) {
           // the next tile's lines into L2, while its buffer is still in use
-          const __nv_bfloat16* nx = tree_row(p, it, off + kTreeTile + row, e);
-          if (nx) prefetch_l2_line(nx + piece * 64);
+          const uint8_t* nx = tree_row(p, it, off + kTreeTile + row, e, &cached);
+          if (nx) prefetch_l2_line(nx + piece * 128);
         }
       }
     }
@@ -372,7 +445,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
       bool stop = false;
       int4 f = tree_info(p, blockIdx.x);
       for (int id = blockIdx.x; id < p.n_items && !stop; id += gridDim.x) {
-        const TreeItem it = tree_item(p, id, f);
+        const TreeItem it = tree_item<kF8>(p, id, f);
         f = tree_info(p, id + gridDim.x);
         if (it.tile1 <= it.tile0) continue;
         if (!mbar_wait_warp(&bar_q_full, icount & 1, &abort_flag)) break;
@@ -414,7 +487,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
       bool stop = false;
       int4 f = tree_info(p, blockIdx.x);
       for (int id = blockIdx.x; id < p.n_items && !stop; id += gridDim.x) {
-        const TreeItem it = tree_item(p, id, f);
+        const TreeItem it = tree_item<kF8>(p, id, f);
         f = tree_info(p, id + gridDim.x);
         for (int tile = it.tile0; tile < it.tile1; ++tile, ++tcount) {
           const int buf = tcount & 1;
@@ -454,7 +527,7 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     const float z2 = p.sinks[h0 + lane] * kLog2e;        // (of head h0 + lane)
     int4 f = tree_info(p, blockIdx.x);
     for (int id = blockIdx.x; id < p.n_items; id += gridDim.x) {
-      const TreeItem it = tree_item(p, id, f);
+      const TreeItem it = tree_item<kF8>(p, id, f);
       f = tree_info(p, id + gridDim.x);
       const bool empty = it.tile1 <= it.tile0;
       bool bad = false;                      // uniform over the group; both groups leave together

@@ -1409,14 +1409,16 @@ int run_tree_compress(const csahca_tree_compress_args* a, void* stream) {
   const bool csa = a->kind == CSAHCA_CSA, f8 = a->out_dtype == CSAHCA_E4M3;
   const int vec = 16 / dtype_size(a->dtype);
   if (!f8 && a->out_dtype != a->dtype) return CSAHCA_ERR_UNSUPPORTED;
+  const int64_t kv_row_bytes = f8 && a->kv_rows ? kv_f8_row_bytes(a->c, a->rope_dims) : 0;
   if (f8 && (a->dtype != CSAHCA_BF16 || a->c % 128)) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->kv_rows && kv_row_bytes == 0) return CSAHCA_ERR_UNSUPPORTED;
   if (a->c % vec || a->c > 128 * vec || a->rope_dims > 2 * kNrMaxPairs) return CSAHCA_ERR_UNSUPPORTED;
   if (a->T > CSAHCA_TREE_MAX_NODES || a->m > kTcpMaxTokens / (csa ? 2 : 1)) return CSAHCA_ERR_UNSUPPORTED;
   if ((int64_t)a->B * a->T > INT32_MAX) return CSAHCA_ERR_UNSUPPORTED;
   if (a->B == 0 || a->T == 0) return CSAHCA_OK;
   if (!a->pos || !a->parents || !a->a || !a->za || !a->ring || !a->bias_a || !a->out) return CSAHCA_ERR_INVALID_ARG;
   if (csa && (!a->b || !a->zb || !a->bias_b)) return CSAHCA_ERR_INVALID_ARG;
-  if (f8 && !a->out_scale) return CSAHCA_ERR_INVALID_ARG;
+  if (f8 && !a->kv_rows && !a->out_scale) return CSAHCA_ERR_INVALID_ARG;
   const void* ptrs[] = {a->pos, a->parents, a->a, a->b, a->za, a->zb, a->ring, a->bias_a, a->bias_b, a->gain,
                         a->out, a->out_scale};
   for (const void* x : ptrs)
@@ -1430,6 +1432,7 @@ int run_tree_compress(const csahca_tree_compress_args* a, void* stream) {
   p.ring = a->ring; p.bias_a = a->bias_a; p.bias_b = a->bias_b; p.gain = a->gain;
   p.out = a->out; p.out_scale = a->out_scale;
   p.T = a->T; p.c = a->c; p.m = a->m; p.rms_norm = a->rms_norm; p.rope_dims = a->rope_dims; p.e4m3 = f8 ? 1 : 0;
+  p.kv_row_bytes = kv_row_bytes;
   p.eps = a->eps > 0 ? a->eps : kDefaultEps;
   rope_theta_pairs(p.theta, a->rope_dims, a->rope_base > 0 ? a->rope_base : kDefaultRopeBase);
   cudaStream_t s = as_stream(stream);
@@ -1468,6 +1471,7 @@ int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
     return CSAHCA_ERR_INVALID_ARG;
   if (a->rope_dims < 0 || a->rope_dims > a->d || (a->rope_dims & 1)) return CSAHCA_ERR_INVALID_ARG;
   if (a->T > CSAHCA_TREE_MAX_NODES || a->d % 32 || a->d > 512) return CSAHCA_ERR_UNSUPPORTED;
+  if (a->kv_dtype == CSAHCA_E4M3 && (!tree_tc(a) || kv_f8_row_bytes(a->d, a->rope_dims) == 0)) return CSAHCA_ERR_UNSUPPORTED;
   // row codes and tensor coordinates are 32-bit
   if ((int64_t)a->B * a->T * a->H > INT32_MAX || a->H > 65535 || (int64_t)a->B * a->N_cap > INT32_MAX ||
       (int64_t)a->B * a->w > kRowMask || (int64_t)a->B * a->T > kRowMask)
@@ -1575,10 +1579,13 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   TreeAttnParams p;
   memset(&p, 0, sizeof(p));
   __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(ws + L.q);
-  p.kv = a->N_cap > 0 ? static_cast<const __nv_bfloat16*>(a->kv_cache) : q;
-  p.rows[ROW_RING] = static_cast<const __nv_bfloat16*>(a->win);
-  p.rows[ROW_TREE] = reinterpret_cast<const __nv_bfloat16*>(ws + L.rows);
-  p.rows[ROW_DRAFT] = static_cast<const __nv_bfloat16*>(a->draft);
+  const bool f8 = a->kv_dtype == CSAHCA_E4M3;
+  p.kv = a->N_cap > 0 ? static_cast<const uint8_t*>(a->kv_cache) : reinterpret_cast<const uint8_t*>(q);
+  p.rows[ROW_RING] = static_cast<const uint8_t*>(a->win);
+  p.rows[ROW_TREE] = reinterpret_cast<const uint8_t*>(ws + L.rows);
+  p.rows[ROW_DRAFT] = static_cast<const uint8_t*>(a->draft);
+  p.row_bytes = f8 ? (int)kv_f8_row_bytes(a->d, a->rope_dims) : 2 * kAttnD;
+  p.nope_chunks = (kAttnD - a->rope_dims) / 64;
   p.idx = sel; p.idx_given = sel && sel == a->idx_in; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
   p.turn = reinterpret_cast<const float2*>(ws + L.turn);
   p.sinks = a->sinks; p.list_stride = a->w + a->T; p.k = a->k; p.N = a->N_cap; p.T = a->T;
@@ -1593,24 +1600,26 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     return CSAHCA_ERR_LAUNCH;
   m_rows = m_q;
   const uint64_t comp_rows = (uint64_t)a->B * a->N_cap;
-  if (!sel && comp_rows >= kTreeTile &&
+  if (!sel && !f8 && comp_rows >= kTreeTile &&
       !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->kv_cache, 64, comp_rows, kAttnChunks, rs, 128, 64,
                  kTreeTile, kTreeHalfChunks, CU_TENSOR_MAP_SWIZZLE_128B))
     return CSAHCA_ERR_LAUNCH;
-  cudaFuncSetAttribute(attn_tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem::TOTAL);
+  auto kern = f8 ? attn_tree_tc_kernel<true> : attn_tree_tc_kernel<false>;
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem::TOTAL);
   // the register split must fit the launch allocation (an increase would wait)
-  static int launch_regs = -1;
-  if (launch_regs < 0) {
+  static int launch_regs[2] = {-1, -1};
+  if (launch_regs[f8] < 0) {
     cudaFuncAttributes fa;
-    launch_regs = cudaFuncGetAttributes(&fa, attn_tree_tc_kernel) == cudaSuccess ? fa.numRegs : 0;
+    launch_regs[f8] = cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
   }
-  if ((int64_t)launch_regs * kTreeThreads <
+  if ((int64_t)launch_regs[f8] * kTreeThreads <
       256 * kAttnRegsSoftmax + 32 * kTreeProducers * kAttnRegsProducer + 128 * kAttnRegsMma)
     return CSAHCA_ERR_UNSUPPORTED;
   const int grid = p.n_items < num_sms() ? p.n_items : num_sms();
   {
-    CSAHCA_TRACE(sel ? "attn_tree_csa_tc" : "attn_tree_hca_tc", s);
-    launch_k(attn_tree_tc_kernel, dim3((unsigned)grid), dim3(kTreeThreads), TreeSmem::TOTAL, s, m_rows, m_q, p);
+    CSAHCA_TRACE(sel ? (f8 ? "attn_tree_csa_tc_f8kv" : "attn_tree_csa_tc")
+                     : (f8 ? "attn_tree_hca_tc_f8kv" : "attn_tree_hca_tc"), s);
+    launch_k(kern, dim3((unsigned)grid), dim3(kTreeThreads), TreeSmem::TOTAL, s, m_rows, m_q, p);
   }
   CSAHCA_CHECK_LAUNCH();
   if (L.splits > 1) {

@@ -38,6 +38,7 @@ struct TreeCompressParams {
   const float* bias_a; const float* bias_b; const float* gain;
   void* out; float* out_scale;          // [B, T, c]; e4m3: codes, [B, T, c / 128]
   int T, c, m, rms_norm, rope_dims, e4m3;
+  int64_t kv_row_bytes;                 // > 0: out holds FP8 KV rows of so many bytes
   float eps;
   double theta[kNrMaxPairs];
 };
@@ -195,6 +196,33 @@ tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
         y[e + 1] = x0 * sn + x1 * cs;
       }
     }
+  }
+  if (p.kv_row_bytes > 0) {
+    // FP8 KV row: 64-dim blocks of codes with one fp32 scale each (the cache's
+    // rule), the rope dims as bf16; 8 lanes hold a block
+    if (tid < (nv + 31) / 32 * 32) {
+      float amax = 0.f;
+      if (tid < nv) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) amax = fmaxf(amax, fabsf(y[e]));
+      }
+#pragma unroll
+      for (int o = 64 / VEC / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      if (tid < nv) {
+        uint8_t* row = static_cast<uint8_t*>(p.out) + (int64_t)tok * p.kv_row_bytes;
+        const int nope = c - p.rope_dims;
+        if (ch0 < nope) {
+          const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            row[ch0 + e] = __nv_cvt_float_to_fp8(__fdiv_rn(y[e], scale), __NV_SATFINITE, __NV_E4M3);
+          if (ch0 % 64 == 0) *reinterpret_cast<float*>(row + c + p.rope_dims + 4 * (ch0 / 64)) = scale;
+        } else {
+          store16(reinterpret_cast<__nv_bfloat16*>(row + nope) + (ch0 - nope), y);
+        }
+      }
+    }
+    return;
   }
   if (!p.e4m3) {
     if (tid < nv) store16(static_cast<T*>(p.out) + (int64_t)tok * c + ch0, y);

@@ -197,9 +197,11 @@ class TreeStep:
             for L in layers:
                 B, T, H, d = L["tq"].shape
                 dev, csa = L["tq"].device, L["kind"] == "csa"
-                draft = torch.zeros(B, T, d, dtype=L["tq"].dtype, device=dev)
+                kv_fp8 = L["kv"].dtype == torch.uint8
+                draft = torch.zeros(B, T, L["kv"].shape[2], dtype=L["kv"].dtype, device=dev)
                 comp = [api.tree_compress_args(L["kind"], L["ts"], L["ring"], L["pos"], L["parents"], L["bias_a"], L["m"],
-                                               bias_b=L["bias_b"], gain=L["kv_gain"], rope_dims=wl.r, out=draft)]
+                                               bias_b=L["bias_b"], gain=L["kv_gain"], rope_dims=wl.r, out=draft,
+                                               kv_fp8=kv_fp8)]
                 kw, idx = {}, None
                 if csa:
                     f8 = L["kI_scale"] is not None

@@ -12,7 +12,7 @@ import numpy as np
 import pytest
 import torch
 
-from long_context_compressed_overlapped_b200 import api
+from long_context_compressed_overlapped_b200 import api, synth
 from oracle import csahca_oracle as O
 from tests import tree_reference as R
 from tests.helpers import check_close, npy
@@ -350,6 +350,59 @@ def test_inactive_sequences_are_left_alone():
     assert (out[1] == 7).all()
     check_attn(s, out)
     assert api.device_error() == 0
+
+
+def pack_fp8(rows, r):
+    """FP8 KV rows of bf16 rows, and the rows they stand for; a row with NaN in
+    it becomes NaN codes, NaN RoPE dims and NaN scales."""
+    bad = rows.isnan().any(-1)
+    packed = synth.pack_kv_rows_fp8(torch.where(bad[..., None], torch.zeros_like(rows), rows), r)
+    packed[bad] = 0xff                                                              # e4m3 and bf16 and fp32 NaN alike
+    codes, scales, rope = synth.unpack_kv_rows_fp8(packed, rows.shape[-1], r)
+    body = codes.contiguous().view(torch.float8_e4m3fn).float().unflatten(-1, (-1, 64)) * scales[..., None]
+    return packed, torch.cat([body.flatten(-2), rope.float()], -1)
+
+
+@pytest.mark.parametrize("r", [64, 128])
+@pytest.mark.parametrize("case", [("hca", 3, 7, [2047, 126, 0], "wide", 128, 128, 0), ("hca", 2, 40, [9000, 77], "padded", 16, 128, 0),
+                                  ("csa", 3, 6, [9000, 10, 0], "wide", 4, 128, 200), ("csa", 1, 64, [5000], "chain", 4, 16, 70)])
+def test_fp8_kv_rows(case, r):
+    """FP8 KV caches and drafted entries, against the oracle on the rows they
+    stand for."""
+    kind, B, T, pos, shape, m, w, k = case
+    s = attn_case(kind, B, T, pos, shape, m, w, k, seed=4, dt=torch.bfloat16, H=64, d=512, r=r)
+    ref = dict(s)
+    s["kv"], ref["kv"] = pack_fp8(s["kv"], r)
+    s["draft"], ref["draft"] = pack_fp8(s["draft"], r)
+    out = run_attn(s, out=torch.full_like(s["q"], 7.0))
+    check_attn(ref, out)
+    assert api.device_error() == 0
+
+
+def test_compress_fp8_kv_rows_are_the_decode_compressors():
+    B, T, d, m, r = 2, 9, 512, 4, 64
+    pos = [1021, 4]
+    s = compress_case("csa", torch.bfloat16, B, T, d, m, pos, "chain", seed=12)
+    rows = run_compress(s, True, r, kv_fp8=True)
+    ring, kv = s["ring"].clone(), torch.zeros(B, 300, 640, dtype=torch.uint8, device=DEV)
+    seen = 0
+    for i in range(T):
+        api.decode_compress("csa", R.ints([x + i for x in pos], DEV), tuple(x[:, i].contiguous() for x in s["streams"]), ring, kv, m=m,
+                            bias_a=s["bias_a"], bias_b=s["bias_b"], kv_gain=s["gain"], rope_dims=r)
+        for b in range(B):
+            if (pos[b] + i + 1) % m == 0:
+                e = (pos[b] + i + 1) // m - 1
+                a, c = synth.unpack_kv_rows_fp8(rows[b, i], d, r), synth.unpack_kv_rows_fp8(kv[b, e], d, r)
+                # pooled in fp32 in different orders: scales to a few ulps, codes and RoPE dims to a step, nearly all equal
+                assert ((a[1] / c[1] - 1).abs() <= 32 * 2.0**-23).all()
+                fa, fc = (x[0].contiguous().view(torch.float8_e4m3fn).float() for x in (a, c))
+                assert (fa - fc).abs().le(torch.maximum(fa.abs(), fc.abs()) * 2.0**-3 + 2.0**-9).all()
+                assert (a[0] == c[0]).float().mean() >= 0.98
+                assert (a[2].float() - c[2].float()).abs().le(c[2].float().abs() * 2.0**-7 + 1e-6).all()
+                seen += 1
+            else:
+                assert (rows[b, i] == 0).all()
+    assert seen == 4
 
 
 def whole(g, lo, hi, dt, *shape):

@@ -59,7 +59,8 @@ def same_selection(tree_idx, seq_idx, path, pos, m, N):
     return len(a ^ b)
 
 
-@pytest.mark.parametrize("name,ctx,B,T", [("decode_256k", 8189, 2, 12), ("decode_1m", 16383, 2, 7), ("decode_1m", 200, 1, 3)])
+@pytest.mark.parametrize("name,ctx,B,T", [("decode_256k", 8189, 2, 12), ("decode_1m", 16383, 2, 7), ("decode_1m", 200, 1, 3),
+                                           ("decode_1m_fp8kv", 16381, 2, 9)])
 def test_step_is_the_decode_steps_of_each_path(name, ctx, B, T):
     wl = synth.WORKLOADS[name]
     layers = synth.tree_inputs(wl, T, DEV, ctx=ctx, B=B, layers=("csa", "hca"), room=2 * T)

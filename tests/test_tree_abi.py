@@ -67,6 +67,8 @@ def comp(**kw):
     (dict(out_dtype=N.E4M3, c=64), N.ERR_UNSUPPORTED),
     (dict(out_dtype=N.E4M3), N.ERR_INVALID_ARG),                                    # no out_scale
     (dict(dtype=N.F32, out_dtype=N.E4M3), N.ERR_UNSUPPORTED),
+    (dict(kv_rows=1), N.ERR_UNSUPPORTED),                                           # FP8 rows are an E4M3 output
+    (dict(out_dtype=N.E4M3, kv_rows=1, c=128, rope_dims=32), N.ERR_UNSUPPORTED),
     (dict(c=132), N.ERR_UNSUPPORTED),
     (dict(T=65), N.ERR_UNSUPPORTED),
     (dict(m=257), N.ERR_UNSUPPORTED),
@@ -104,6 +106,9 @@ INDEXER = dict(idx_in=None, HI=4, dI=128, qI_dtype=N.BF16, kI_dtype=N.BF16, qI=6
     (dict(T=65), N.ERR_UNSUPPORTED),
     (dict(d=48, rope_dims=0), N.ERR_UNSUPPORTED),
     (dict(d=544), N.ERR_UNSUPPORTED),
+    (dict(kv_dtype=N.E4M3, d=128), N.ERR_UNSUPPORTED),
+    (dict(kv_dtype=N.E4M3, rope_dims=32), N.ERR_UNSUPPORTED),
+    (dict(kv_dtype=N.E4M3, dtype=N.F32), N.ERR_UNSUPPORTED),
     (dict(k=0), N.ERR_INVALID_ARG),
     (dict(k=2**31 - 1), N.ERR_UNSUPPORTED),
     (dict(N_cap=2**31 - 1), N.ERR_UNSUPPORTED),
