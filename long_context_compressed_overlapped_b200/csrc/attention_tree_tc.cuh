@@ -220,6 +220,37 @@ __device__ __forceinline__ uint4 f8x8_to_bf16(uint2 codes, float scale) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// FP8 KV rows of a sequence's committed entries and of its drafted ones, as the
+// bf16 rows they stand for: HCA calls of several nodes a sequence read every
+// entry once a node, so that widening them once and running the bf16 kernel
+// costs less than widening in every gather.  64 threads a row, 8 dims each;
+// bound by HBM.
+struct KvWidenParams {
+  const uint8_t* kv; const uint8_t* draft; const int* pos;
+  __nv_bfloat16* kv_out; __nv_bfloat16* draft_out;     // [B, N, D], [B, T, D]
+  int B, N, T, m, row_bytes, rope_dims;
+};
+__global__ void __launch_bounds__(256) kv_widen_kernel(const __grid_constant__ KvWidenParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.y, v = p.pos[b] < 0 ? 0 : min(p.N, p.pos[b] / p.m);
+  const int rows = v + (p.draft ? p.T : 0), piece = threadIdx.x & 63, chunk = piece >> 3;
+  const int nope = (kAttnD - p.rope_dims) / 64;
+  for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4) {
+    const uint8_t* src = r < v ? p.kv + ((int64_t)b * p.N + r) * p.row_bytes
+                               : p.draft + ((int64_t)b * p.T + (r - v)) * p.row_bytes;
+    uint4 w;
+    if (chunk < nope)
+      w = f8x8_to_bf16(__ldg(reinterpret_cast<const uint2*>(src + piece * 8)),
+                       __ldg(reinterpret_cast<const float*>(src + kAttnD + p.rope_dims + 4 * chunk)));
+    else
+      w = __ldg(reinterpret_cast<const uint4*>(src + nope * 64 + (piece - 8 * nope) * 16));
+    __nv_bfloat16* dst = r < v ? p.kv_out + ((int64_t)b * p.N + r) * kAttnD
+                               : p.draft_out + ((int64_t)b * p.T + (r - v)) * kAttnD;
+    *reinterpret_cast<uint4*>(dst + piece * 8) = w;
+  }
+}
+
 // kF8: the cache and the drafted entries are FP8 KV rows.  Every tile is
 // gathered, and the producers widen the codes to bf16 between the load and the
 // shared-memory row (through registers, half a tile at a time), as a row stands

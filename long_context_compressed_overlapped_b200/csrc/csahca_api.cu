@@ -1506,8 +1506,8 @@ int validate_tree(const csahca_tree_attn_args* a, bool shapes_only = false) {
 }
 
 struct TreeLayout {
-  size_t node_pos, sel_pos, info, turn, list, rows, q, sel_scores, idx, indexer, indexer_bytes, partial, total;
-  bool tc;
+  size_t node_pos, sel_pos, info, turn, list, rows, q, wide_kv, wide_draft, sel_scores, idx, indexer, indexer_bytes, partial, total;
+  bool tc, widen;
   int splits;
 };
 
@@ -1526,6 +1526,15 @@ int tree_splits(int64_t nodes, int tiles) {
   return best;
 }
 
+// HCA calls of four nodes a sequence and more widen an FP8 KV cache into the
+// workspace first.  A layer's step, widened first / in each gather, 4 sequences:
+// 8,192 entries, 1 node 48 / 44 us, 2 nodes 51 / 55, 4 nodes 59 / 76, 16 nodes
+// 133 / 251; 512 entries, 2 nodes 26.7 / 24.6, 4 nodes 28.7 / 28.6, 16 nodes
+// 39 / 44.  (CSA gathers other rows for each node: widened in the gather.)
+bool tree_widens(const csahca_tree_attn_args* a) {
+  return a->kind == CSAHCA_HCA && a->kv_dtype == CSAHCA_E4M3 && a->T >= 4 && a->N_cap > 0;
+}
+
 TreeLayout tree_layout(const csahca_tree_attn_args* a) {
   TreeLayout L;
   const bool csa = a->kind == CSAHCA_CSA;
@@ -1541,6 +1550,9 @@ TreeLayout tree_layout(const csahca_tree_attn_args* a) {
   L.list = take((size_t)nodes * (a->w + a->T) * 4);
   L.rows = take(nodes * a->d * e);
   L.q = L.tc ? take((size_t)nodes * a->H * a->d * e) : off;
+  L.widen = tree_widens(a);
+  L.wide_kv = L.widen ? take((size_t)a->B * a->N_cap * a->d * e) : off;
+  L.wide_draft = L.widen && a->draft ? take(nodes * a->d * e) : off;
   const bool select = csa && !a->idx_in;
   L.sel_scores = select && a->draft_kI ? take((size_t)nodes * a->k * 4) : off;
   L.idx = select && !a->idx_out ? take((size_t)nodes * a->k * 4) : off;
@@ -1579,11 +1591,30 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   TreeAttnParams p;
   memset(&p, 0, sizeof(p));
   __nv_bfloat16* q = reinterpret_cast<__nv_bfloat16*>(ws + L.q);
-  const bool f8 = a->kv_dtype == CSAHCA_E4M3;
-  p.kv = a->N_cap > 0 ? static_cast<const uint8_t*>(a->kv_cache) : reinterpret_cast<const uint8_t*>(q);
+  const bool f8 = a->kv_dtype == CSAHCA_E4M3 && !L.widen;
+  const void* cache = a->kv_cache;
+  const void* draft = a->draft;
+  if (L.widen) {
+    KvWidenParams wp;
+    memset(&wp, 0, sizeof(wp));
+    wp.kv = static_cast<const uint8_t*>(a->kv_cache); wp.draft = static_cast<const uint8_t*>(a->draft); wp.pos = a->pos;
+    wp.kv_out = reinterpret_cast<__nv_bfloat16*>(ws + L.wide_kv);
+    wp.draft_out = reinterpret_cast<__nv_bfloat16*>(ws + L.wide_draft);
+    wp.B = a->B; wp.N = a->N_cap; wp.T = a->T; wp.m = a->m; wp.rope_dims = a->rope_dims;
+    wp.row_bytes = (int)kv_f8_row_bytes(a->d, a->rope_dims);
+    int64_t per = ceil_div64(a->N_cap + a->T, 16);        // (four turns of a CTA's four rows)
+    const int64_t most = ceil_div64(16 * num_sms(), a->B);
+    if (per > most) per = most;
+    CSAHCA_TRACE("kv_widen", s);
+    launch_k(kv_widen_kernel, dim3((unsigned)per, (unsigned)a->B), dim3(256), 0, s, wp);
+    CSAHCA_CHECK_LAUNCH();
+    cache = wp.kv_out;
+    draft = a->draft ? wp.draft_out : nullptr;
+  }
+  p.kv = a->N_cap > 0 ? static_cast<const uint8_t*>(cache) : reinterpret_cast<const uint8_t*>(q);
   p.rows[ROW_RING] = static_cast<const uint8_t*>(a->win);
   p.rows[ROW_TREE] = reinterpret_cast<const uint8_t*>(ws + L.rows);
-  p.rows[ROW_DRAFT] = static_cast<const uint8_t*>(a->draft);
+  p.rows[ROW_DRAFT] = static_cast<const uint8_t*>(draft);
   p.row_bytes = f8 ? (int)kv_f8_row_bytes(a->d, a->rope_dims) : 2 * kAttnD;
   p.nope_chunks = (kAttnD - a->rope_dims) / 64;
   p.idx = sel; p.idx_given = sel && sel == a->idx_in; p.list = reinterpret_cast<const int*>(ws + L.list); p.info = reinterpret_cast<const int4*>(ws + L.info);
@@ -1601,7 +1632,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
   m_rows = m_q;
   const uint64_t comp_rows = (uint64_t)a->B * a->N_cap;
   if (!sel && !f8 && comp_rows >= kTreeTile &&
-      !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a->kv_cache, 64, comp_rows, kAttnChunks, rs, 128, 64,
+      !encode_3d(&m_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cache, 64, comp_rows, kAttnChunks, rs, 128, 64,
                  kTreeTile, kTreeHalfChunks, CU_TENSOR_MAP_SWIZZLE_128B))
     return CSAHCA_ERR_LAUNCH;
   auto kern = f8 ? attn_tree_tc_kernel<true> : attn_tree_tc_kernel<false>;

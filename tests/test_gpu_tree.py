@@ -365,6 +365,7 @@ def pack_fp8(rows, r):
 
 @pytest.mark.parametrize("r", [64, 128])
 @pytest.mark.parametrize("case", [("hca", 3, 7, [2047, 126, 0], "wide", 128, 128, 0), ("hca", 2, 40, [9000, 77], "padded", 16, 128, 0),
+                                  ("hca", 2, 3, [2047, 600], "chain", 16, 16, 0),        # (few nodes: widened in the gather)
                                   ("csa", 3, 6, [9000, 10, 0], "wide", 4, 128, 200), ("csa", 1, 64, [5000], "chain", 4, 16, 70)])
 def test_fp8_kv_rows(case, r):
     """FP8 KV caches and drafted entries, against the oracle on the rows they
