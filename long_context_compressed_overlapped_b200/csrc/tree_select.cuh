@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   const int free_places = p.k - valid_s;
   int y = 0;
   for (int x = 0; x < nd; ++x) y += free_places + below[x] > rank_s[x];
+  if (y == 0) return;                                // (uniform) the selection stays as it is
   for (int drop = y - free_places; drop > 0; --drop) {
     // the lowest candidate left: (score, higher index first)
     unsigned long long mn = ~0ull;
