@@ -235,14 +235,19 @@ class TreeStep:
         """Take the accepted tokens into every layer's compressors, caches and
         window: paths [B, n] holds each sequence's accepted nodes from the first
         drafted token down, -1 behind the last.  One decode_compress a depth and
-        layer; L["pos"] moves on by the accepted tokens."""
+        layer; L["pos"] moves on by the accepted tokens.  Runs on the step's
+        stream, behind what the current one (which made `paths`) holds; sequences
+        without committed tokens to follow (pos < 0) stay as they are."""
+        self.stream.wait_stream(torch.cuda.current_stream(self.stream.device))
         with torch.cuda.stream(self.stream):
+            if paths.is_cuda:
+                paths.record_stream(self.stream)
             paths = paths.to(self.stream.device, torch.int64)
             for L in self.layers:
                 csa = L["kind"] == "csa"
                 for j in range(paths.shape[1]):
                     node = paths[:, j]
-                    pos = torch.where(node >= 0, L["pos"] + j, torch.full_like(L["pos"], -1))
+                    pos = torch.where((node >= 0) & (L["pos"] >= 0), L["pos"] + j, -1)
 
                     def take(x):
                         return x[torch.arange(x.shape[0], device=x.device), node.clamp(min=0)].contiguous()
@@ -254,7 +259,7 @@ class TreeStep:
                                         bias_a=L["bias_a"], bias_b=L["bias_b"], kv_raw=take(L["tkv_raw"]), win=L["win"],
                                         kv_gain=L["kv_gain"], rope_dims=self.wl.r, stream=self.stream, **kw)
             for L in self.layers:
-                L["pos"] += (paths >= 0).sum(1).to(L["pos"].dtype)
+                L["pos"] += ((paths >= 0).sum(1) * (L["pos"] >= 0)).to(L["pos"].dtype)
 
 
 class HostIOGraph:

@@ -112,3 +112,32 @@ def test_step_is_the_decode_steps_of_each_path(name, ctx, B, T):
             continue
         check_close(npy(step.outputs[li][0, T - 1]), npy(outs[-1][0]), "bf16", f"next step, layer {li}")
     assert api.device_error() == 0
+
+
+def test_commit_leaves_inactive_sequences_alone():
+    """Nodes named for a sequence without committed tokens are not taken, and
+    paths made on the current stream are waited for."""
+    wl = synth.WORKLOADS["decode_1m"]
+    layers = synth.tree_inputs(wl, 3, DEV, ctx=254, B=2, layers=("csa", "hca"), room=6)
+    for L in layers:
+        L["pos"][0] = -1
+    before = clone(layers)
+    step = runtime.TreeStep(wl, layers, torch.cuda.Stream())
+    step()
+    slow = torch.randn(4096, 4096, device=DEV)
+    for _ in range(8):
+        slow = slow @ slow * 1e-3
+    path = R.path_of(layers[0]["parents"].tolist()[1], 2)
+    paths = torch.full((2, len(path)), -1, device=DEV, dtype=torch.int32)
+    paths[0] = 0
+    paths[1] = R.ints(path, DEV)
+    step.commit(paths)
+    step.stream.synchronize()
+    for li, (L, was) in enumerate(zip(layers, before)):
+        _, _, one = decode_path(wl, was, 1, path, 254)
+        assert L["pos"].tolist() == [-1, 254 + len(path)]
+        for key in ("kv", "win", "ring", "iring", "kI", "kI_scale"):
+            if L.get(key) is not None:
+                assert torch.equal(L[key][0], was[key][0]), f"layer {li} {key} of the inactive sequence"
+                assert torch.equal(L[key][1], one[key][0]), f"layer {li} {key}"
+    assert api.device_error() == 0
