@@ -490,10 +490,12 @@ int cp_attn_merge(const csahca_cp_merge_args* args, void* stream);
  * Finished key rows are what the caches and the window ring hold.
  * Layout: q [B, n, HQ, d], k [B, n, HK, d] with the dims of a head contiguous
  *   and the batch, token and head strides of q_stride / k_stride (in elements,
- *   multiples of 16 bytes, >= 0; all three 0: contiguous), so that heads may be
- *   slices of one projection or broadcast along some of the three; pos [B, n] int32 on the device; gains [d] f32;
+ *   multiples of 16 bytes, >= 0; all three 0: contiguous; that of a dim of size
+ *   1 is not used), so that heads may be slices of one projection or broadcast
+ *   along some of the three; pos [B, n] int32 on the device; gains [d] f32;
  *   q_out [B, n, HQ, d], k_out [B, n, HK, d] contiguous (either may be its own
- *   input where that is contiguous).  HQ or HK = 0: that side is left out.
+ *   input where that is contiguous; else they overlap no input and not each
+ *   other).  HQ or HK = 0: that side is left out.
  *   The rows of a token with pos < 0 (padding) are left as they were.
  * Constraints: dtype F32 (d % 4 == 0, d <= 512) or BF16 (d % 8 == 0, d <=
  *   1024); rope_dims even, <= d and <= 512, (d - rope_dims) even.  No
@@ -597,7 +599,8 @@ int tree_compress(const csahca_tree_compress_args* args, void* stream);
  *   score, ties to the lower index.  draft_kI [B, T, dI] (kI_dtype; E4M3 with
  *   draft_kI_scale [B, T, dI / 128]) are the drafted entries' indexer keys
  *   (tree_compress of the indexer streams).  idx_out [B, T, k] (optional)
- *   receives the selection, ascending and -1 padded.
+ *   receives the selection, ascending and -1 padded (-1 where there is no node);
+ *   with idx_in, a copy of it.
  * draft [B, T, d] holds tree_compress's rows; NULL: drafted entries are no keys.
  * Layout: q, out [B, T, H, d]; kv_cache [B, N_cap, d]; win [B, w, d]; kv_raw
  *   [B, T, d]; pos [B], parents [B, T]; gains [d] f32 or NULL (ones); sinks [H].
@@ -608,7 +611,9 @@ int tree_compress(const csahca_tree_compress_args* args, void* stream);
  *   128, else CSAHCA_ERR_UNSUPPORTED.  Any other kv_dtype: rows of `dtype`.
  * Constraints: d % 32 == 0, d <= 512; rope_dims even, <= d; k <= 4096 where
  *   draft_kI is given.
- * Workspace: csahca_tree_workspace_size(). */
+ * Workspace: csahca_tree_workspace_size() of the same struct, which looks at
+ *   the sizes and at which of draft, idx_in, idx_out and draft_kI are given (HCA
+ *   calls of several nodes over FP8 KV rows keep the cache as bf16 rows there). */
 typedef struct {
   int32_t kind;
   int32_t dtype;

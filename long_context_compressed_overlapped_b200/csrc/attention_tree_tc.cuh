@@ -17,8 +17,9 @@
 // per 128 keys.  With all SMs at work a tile takes some 3,000 cycles: 64 KB a
 // tile and node is 5.9 TB/s out of L2, near the 7.3 to 7.7 TB/s that a bare
 // stream of boxes reaches, so the tiles' way out of L2 bounds HCA calls of many
-// nodes (64 nodes over 8,192 entries: 119 us for 0.56 GB; dealing the tiles out
-// evenly over all SMs instead of two items a node changed nothing).  A CTA
+// nodes (64 nodes over 8,192 entries: 106 us for 0.56 GB, start and end included;
+// dealing the tiles out evenly over all SMs instead of two items a node changed
+// nothing).  A CTA
 // cannot keep two nodes: O^T of one is half of TMEM.
 //
 // A node's keys are two runs.  Tiles of 64 consecutive committed entries
@@ -233,10 +234,10 @@ struct KvWidenParams {
 __global__ void __launch_bounds__(256) kv_widen_kernel(const __grid_constant__ KvWidenParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.y, v = p.pos[b] < 0 ? 0 : min(p.N, p.pos[b] / p.m);
+  const int b = blockIdx.x, v = p.pos[b] < 0 ? 0 : min(p.N, p.pos[b] / p.m);
   const int rows = v + (p.draft ? p.T : 0), piece = threadIdx.x & 63, chunk = piece >> 3;
   const int nope = (kAttnD - p.rope_dims) / 64;
-  for (int r = blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += gridDim.x * 4) {
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 6); r < rows; r += gridDim.y * 4) {
     const uint8_t* src = r < v ? p.kv + ((int64_t)b * p.N + r) * p.row_bytes
                                : p.draft + ((int64_t)b * p.T + (r - v)) * p.row_bytes;
     uint4 w;
@@ -309,7 +310,8 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
     const int tiles = (p.k + p.list_stride - p.T + kTreeTile - 1) / kTreeTile;
     const int j = tree_tile0(tiles, blockIdx.x - node * p.splits, p.splits) * kTreeTile + 4 * (warp - 8) + (lane >> 3);
     const int e = j < p.k ? __ldg(p.idx + (int64_t)node * p.k + j) : -1;
-    if (e >= 0 && e < p.N) prefetch_l2_line(p.kv + ((int64_t)(node / p.T) * p.N + e) * p.row_bytes + min((lane & 7) * 128, p.row_bytes - 16));
+    if (e >= 0 && e < p.N)
+      prefetch_l2_line(p.kv + ((int64_t)(node / p.T) * p.N + e) * p.row_bytes + min((lane & 7) * 128, p.row_bytes - 16));
   }
   griddep_wait();
   griddep_launch_dependents();

@@ -1358,11 +1358,13 @@ int run_norm_rope(const csahca_norm_rope_args* a, void* stream) {
   for (int k = 0; k < 2; ++k) {
     const int64_t own[3] = {(int64_t)a->n * p.heads[k] * a->d, (int64_t)p.heads[k] * a->d, a->d};
     const bool dense = !st[k][0] && !st[k][1] && !st[k][2];
+    const int size[3] = {a->B, a->n, p.heads[k]};
     bool same = true;
     for (int x = 0; x < 3; ++x) {
-      if (st[k][x] < 0) return CSAHCA_ERR_INVALID_ARG;
-      if (st[k][x] % vec) return CSAHCA_ERR_ALIGNMENT;
-      p.xs[k][x] = dense ? own[x] : st[k][x];
+      const bool step = !dense && size[x] > 1;          // (a stride that no row is reached by says nothing)
+      if (step && st[k][x] < 0) return CSAHCA_ERR_INVALID_ARG;
+      if (step && st[k][x] % vec) return CSAHCA_ERR_ALIGNMENT;
+      p.xs[k][x] = step ? st[k][x] : own[x];
       p.ys[k][x] = own[x];
       same = same && p.xs[k][x] == own[x];
     }
@@ -1606,7 +1608,7 @@ int launch_tree_tc(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws
     const int64_t most = ceil_div64(16 * num_sms(), a->B);
     if (per > most) per = most;
     CSAHCA_TRACE("kv_widen", s);
-    launch_k(kv_widen_kernel, dim3((unsigned)per, (unsigned)a->B), dim3(256), 0, s, wp);
+    launch_k(kv_widen_kernel, dim3((unsigned)a->B, (unsigned)per), dim3(256), 0, s, wp);
     CSAHCA_CHECK_LAUNCH();
     cache = wp.kv_out;
     draft = a->draft ? wp.draft_out : nullptr;

@@ -111,6 +111,25 @@ def test_broadcast_rows():
         check(y, reference(x.expand(2, 3, 5, 64), pos, 16, None, True), torch.float32, 64, np.ones((2, 3), bool))
 
 
+def test_strides_of_dims_of_size_one():
+    """A dim of size 1 may carry any stride; in place is contiguous all the same."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    base = torch.randn(4096, generator=g, device=DEV)
+    pos = torch.arange(3, device=DEV, dtype=torch.int32).view(1, 3) * 501
+    x = base.as_strided((1, 3, 2, 64), (7, 256, 96, 1))
+    y, _ = api.qk_norm_rope(x, None, pos, rope_dims=16)
+    check(y, reference(x, pos, 16, None, True), torch.float32, 64, np.ones((1, 3), bool))
+    x = base.as_strided((3, 1, 1, 64), (128, 13, 5, 1))
+    y, _ = api.qk_norm_rope(x, None, pos.view(3, 1), rope_dims=16)
+    check(y, reference(x, pos.view(3, 1), 16, None, True), torch.float32, 64, np.ones((3, 1), bool))
+    x = base.clone().as_strided((1, 1, 2, 64), (9, 11, 64, 1))
+    ref = reference(x, pos[:, 1:2], 16, None, True)
+    with pytest.raises(RuntimeError):                       # (positions at an address that is no multiple of 16)
+        api.qk_norm_rope(x, None, pos[:, 1:2], rope_dims=16, q_out=x)
+    y, _ = api.qk_norm_rope(x, None, pos[:, 1:2].clone(), rope_dims=16, q_out=x)
+    check(y, ref, torch.float32, 64, np.ones((1, 1), bool))
+
+
 def test_zero_rows_and_large_rows():
     x = torch.zeros(1, 3, 2, 64, device=DEV)
     x[0, 1] = 1e15

@@ -329,6 +329,16 @@ def test_selection_with_holes_and_bad_entries(heads):
     check_attn(s, out, idx=clean)
 
 
+@pytest.mark.parametrize("heads", [SMALL, TC], ids=["f32", "tc"])
+def test_an_entry_named_twice_is_two_keys(heads):
+    s = attn_case("csa", 1, 3, [2000], "chain", 4, 16, 150, **heads)
+    s["idx"][0, :, 70:90] = s["idx"][0, :, 10:30].clone()
+    s["idx"][0, 1] = s["idx"][0, 1, 3]
+    out = run_attn(s)
+    check_attn(s, out)
+    assert api.device_error() == 0
+
+
 def test_bad_parent_is_reported():
     s = attn_case("hca", 1, 5, [300], "chain", 128, 16, **SMALL)
     s["parents"][0][2] = 2                                                          # its own parent: a walk that must end
