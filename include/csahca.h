@@ -532,7 +532,8 @@ int qk_norm_rope(const csahca_norm_rope_args* args, void* stream);
  * by one: the committed entries (pos[b] / m of them), the entries that the path
  * itself completes, and the window over ring and path.
  *   The rows of places without a node, of nodes below one, and of sequences
- *   with pos[b] < 0 are left as they were.  A parent that is not below its
+ *   with pos[b] < 0 are left as they were, or with zero_rest != 0 written as
+ *   zeros (tree_compress: those of nodes that complete nothing, too).  A parent that is not below its
  *   child raises device error 2 and the node counts as none.
  * Constraints of both calls: 0 <= T <= CSAHCA_TREE_MAX_NODES; positions below
  * 2^31 - 64. */
@@ -565,6 +566,8 @@ typedef struct {
   float rope_base;     /* 0 -> 10000 */
   float eps;           /* 0 -> 1e-6 */
   int32_t kv_rows;     /* out_dtype E4M3: FP8 KV rows */
+  int32_t zero_rest;   /* what no entry fills of out becomes zeros (out_scale is left) */
+  int32_t reserved0;
   const int32_t* pos;
   const int32_t* parents;
   const void* a;
@@ -630,7 +633,7 @@ typedef struct {
   int32_t HI, dI;
   int32_t qI_dtype, kI_dtype;
   int32_t kv_dtype;    /* CSAHCA_E4M3: FP8 KV rows; else rows of dtype */
-  int32_t reserved0;
+  int32_t zero_rest;   /* rows of out without a node become zeros */
   const void* q;
   const int32_t* pos;
   const int32_t* parents;

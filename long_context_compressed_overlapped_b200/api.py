@@ -418,12 +418,14 @@ def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=N
     f8 = kv_fp8 or out_scale is not None
     odt = torch.uint8 if f8 else dt
     oshape = (B, T, N.lib().csahca_kv_row_bytes(N.E4M3, c, rope_dims)) if kv_fp8 else shape
-    if out is None:
-        out = torch.zeros(oshape, dtype=odt, device=dev)
+    fresh = out is None
+    if fresh:
+        out = torch.empty(oshape, dtype=odt, device=dev)
     p = [_arg("streams", t, dev, shape, dt) for t in streams]
     a = N.TreeCompressArgs(
         kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
         rms_norm=bool(rms_norm), rope_dims=rope_dims, rope_base=rope_base, eps=eps, kv_rows=bool(kv_fp8),
+        zero_rest=fresh,
         pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
         a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
         ring=_arg("ring", ring, dev, (B, 2 * m, 4, c) if csa else (B, m, 2, c), dt),
@@ -449,7 +451,7 @@ def tree_compress(kind, streams, ring, pos, parents, bias_a, m, *, stream=None, 
     pos [B] the first drafted token's position; parents [B, T] (parent node, -1
     for a node that follows the last committed token, < -1 for no node).
     out [B, T, c]: row i is written iff node i's token ends a block, the others
-    are left as they were (a new out starts at zero).  With out_scale
+    are left as they were (zero in a new out).  With out_scale
     [B, T, c / 128] f32, out holds e4m3 codes (uint8), as for indexer keys; with
     kv_fp8, FP8 KV rows (uint8 [B, T, csahca_kv_row_bytes]).
     bias_b, gain, rms_norm, rope_dims, rope_base, eps as in csa_compress."""
@@ -471,8 +473,9 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     B, T, H, d = shape
     Nc = kv_cache.shape[1]
     w = win.shape[1] if win is not None else 0
-    if out is None:
-        out = torch.zeros(shape, dtype=dt, device=dev)
+    fresh = out is None
+    if fresh:
+        out = torch.empty(shape, dtype=dt, device=dev)
     row = (B, T, d)
     # a uint8 cache holds FP8 KV rows, and so do the drafted entries
     f8 = kv_cache.dtype is torch.uint8
@@ -480,7 +483,7 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     # (in the struct's order)
     a = N.TreeAttnArgs(
         N.CSA if csa else N.HCA, code, B, T, H, d, Nc, m, w, k, rope_dims, rope_base, eps, scale, bool(q_norm),
-        bool(kv_norm), 0, 0, 0, 0, N.E4M3 if f8 else code, 0,
+        bool(kv_norm), 0, 0, 0, 0, N.E4M3 if f8 else code, fresh,
         _arg("q", q, dev, shape, dt), _ints("pos", pos, dev, (B,), keep), _ints("parents", parents, dev, (B, T), keep),
         None if q_gain is None else _floats("q_gain", q_gain, dev, (d,), keep),
         None if kv_gain is None else _floats("kv_gain", kv_gain, dev, (d,), keep),
@@ -542,7 +545,7 @@ def compressed_attn_tree(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *,
     CSA: idx_in [B, T, k] (N_cap + j names draft row j), or k with qI, wI, kI
     (kI_scale) and draft_kI (draft_kI_scale) for the lightning indexer; idx_out
     [B, T, k] receives the selection.  Rows of places without a node are left as
-    they were (a new out starts at zero).  Returns out [B, T, H, d]."""
+    they were (zero in a new out).  Returns out [B, T, H, d]."""
     return _on(stream, q.device, _attn_tree, (kind, q, pos, parents, kv_cache, win, kv_raw, sinks),
                dict(kw, m=m, rope_dims=rope_dims), workspace)
 

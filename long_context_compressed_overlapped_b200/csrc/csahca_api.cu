@@ -1435,6 +1435,8 @@ int run_tree_compress(const csahca_tree_compress_args* a, void* stream) {
   p.out = a->out; p.out_scale = a->out_scale;
   p.T = a->T; p.c = a->c; p.m = a->m; p.rms_norm = a->rms_norm; p.rope_dims = a->rope_dims; p.e4m3 = f8 ? 1 : 0;
   p.kv_row_bytes = kv_row_bytes;
+  p.zero_rest = a->zero_rest;
+  p.out_row_bytes = kv_row_bytes > 0 ? kv_row_bytes : (int64_t)a->c * dtype_size(a->out_dtype);
   p.eps = a->eps > 0 ? a->eps : kDefaultEps;
   rope_theta_pairs(p.theta, a->rope_dims, a->rope_base > 0 ? a->rope_base : kDefaultRopeBase);
   cudaStream_t s = as_stream(stream);
@@ -1715,6 +1717,8 @@ int run_tree_t(const csahca_tree_attn_args* a, const TreeLayout& L, char* ws, cu
     t.list_drafts = !csa && a->draft ? 1 : 0;
     t.node_pos = node_pos; t.sel_pos = sel_pos; t.list = list; t.info = info;
     t.turn = L.tc ? reinterpret_cast<float2*>(ws + L.turn) : nullptr;
+    t.zero = a->zero_rest ? static_cast<uint4*>(a->out) : nullptr;
+    t.zero_n = (int)((int64_t)a->H * a->d * sizeof(T) / 16);      // (H <= 65535, d <= 512)
     rope_theta_pairs(p.theta, a->rope_dims, base);
     st = launch_norm_rope<T, true>(p, nodes, s);
     if (st != CSAHCA_OK) return st;

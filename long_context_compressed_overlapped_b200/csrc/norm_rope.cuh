@@ -46,6 +46,8 @@ struct TreePlan {
   int* list;                // [B, T][w + T] row codes
   int4* info;               // [B, T] {position, visible committed entries, length of the list, 0}
   float2* turn;             // [B, T][r / 2] cos, sin of the node's angles (optional)
+  uint4* zero;              // [B, T][zero_n]: rows of places without a node become zeros (optional)
+  int zero_n;
 };
 
 struct NormRopeParams {
@@ -258,7 +260,14 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
       }
       if (threadIdx.x == 0) L.info[tok0] = make_int4(t, t < 0 ? 0 : min(L.N, p0 / L.m), count, 0);
     }
-    if (t < 0) return;
+    if (t < 0) {
+      if (p.plan.zero) {
+        uint4* z = p.plan.zero + (int64_t)tok0 * p.plan.zero_n;
+        for (int j = blockIdx.y * blockDim.x + threadIdx.x; j < p.plan.zero_n; j += gridDim.y * blockDim.x)
+          z[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      return;
+    }
     if (threadIdx.x == 0) pos_s[0] = t;
   } else {
     if (threadIdx.x < p.tpc) pos_s[threadIdx.x] = tok0 + threadIdx.x < p.tokens ? p.pos[tok0 + threadIdx.x] : -1;

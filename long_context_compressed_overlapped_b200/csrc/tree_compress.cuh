@@ -39,6 +39,7 @@ struct TreeCompressParams {
   void* out; float* out_scale;          // [B, T, c]; e4m3: codes, [B, T, c / 128]
   int T, c, m, rms_norm, rope_dims, e4m3;
   int64_t kv_row_bytes;                 // > 0: out holds FP8 KV rows of so many bytes
+  int64_t out_row_bytes; int zero_rest; // rows that no entry fills become zeros
   float eps;
   double theta[kNrMaxPairs];
 };
@@ -62,7 +63,12 @@ tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
   const int tok = blockIdx.x, b = tok / p.T, i = tok - b * p.T;
   const int t = tree_node(p.parents, p.pos, b, p.T, i, &node_s);
   const int m = p.m, c = p.c;
-  if (t < 0 || (t + 1) % m != 0) return;
+  if (t < 0 || (t + 1) % m != 0) {
+    // (a row of out is a multiple of 8 bytes: c % 128 codes, 16-byte vectors, or an FP8 KV row)
+    uint2* z = p.zero_rest ? reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + tok * p.out_row_bytes) : nullptr;
+    for (int j = threadIdx.x; z && j < (int)(p.out_row_bytes / 8); j += kThreads) z[j] = make_uint2(0u, 0u);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31;
   const int R = kCSA ? 2 * m : m;
   const int p0 = node_s.pos0;
@@ -200,6 +206,11 @@ tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
   if (p.kv_row_bytes > 0) {
     // FP8 KV row: 64-dim blocks of codes with one fp32 scale each (the cache's
     // rule), the rope dims as bf16; 8 lanes hold a block
+    if (p.zero_rest) {                                // (and what fills the row up to 128 bytes)
+      uint32_t* row = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + tok * p.kv_row_bytes);
+      for (int j = (c + p.rope_dims) / 4 + (c - p.rope_dims) / 64 + tid; j < (int)(p.kv_row_bytes / 4); j += kThreads)
+        row[j] = 0u;
+    }
     if (tid < (nv + 31) / 32 * 32) {
       float amax = 0.f;
       if (tid < nv) {

@@ -103,7 +103,7 @@ class NormRopeArgs(C.Structure):
 class TreeCompressArgs(C.Structure):
     _fields_ = [("kind", i32), ("dtype", i32), ("out_dtype", i32), ("B", i32), ("T", i32), ("c", i32),
                 ("m", i32), ("rms_norm", i32), ("rope_dims", i32), ("rope_base", f32), ("eps", f32),
-                ("kv_rows", i32), ("pos", vp), ("parents", vp), ("a", vp), ("b", vp), ("za", vp),
+                ("kv_rows", i32), ("zero_rest", i32), ("reserved0", i32), ("pos", vp), ("parents", vp), ("a", vp), ("b", vp), ("za", vp),
                 ("zb", vp), ("ring", vp), ("bias_a", vp), ("bias_b", vp), ("gain", vp), ("out", vp),
                 ("out_scale", vp)]
 
@@ -112,7 +112,7 @@ class TreeAttnArgs(C.Structure):
     _fields_ = [("kind", i32), ("dtype", i32), ("B", i32), ("T", i32), ("H", i32), ("d", i32),
                 ("N_cap", i32), ("m", i32), ("w", i32), ("k", i32), ("rope_dims", i32),
                 ("rope_base", f32), ("eps", f32), ("scale", f32), ("q_norm", i32), ("kv_norm", i32),
-                ("HI", i32), ("dI", i32), ("qI_dtype", i32), ("kI_dtype", i32), ("kv_dtype", i32), ("reserved0", i32),
+                ("HI", i32), ("dI", i32), ("qI_dtype", i32), ("kI_dtype", i32), ("kv_dtype", i32), ("zero_rest", i32),
                 ("q", vp), ("pos", vp), ("parents", vp), ("q_gain", vp), ("kv_gain", vp),
                 ("kv_cache", vp), ("win", vp), ("kv_raw", vp), ("draft", vp), ("sinks", vp), ("qI", vp),
                 ("wI", vp), ("kI", vp), ("kI_scale", vp), ("draft_kI", vp), ("draft_kI_scale", vp),

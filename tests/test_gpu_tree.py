@@ -522,6 +522,41 @@ def test_streams_graphs_and_workspaces(kind):
     assert api.device_error() == 0
 
 
+@pytest.mark.parametrize("heads", [SMALL, TC, HEADS16], ids=["f32", "tc", "16h"])
+@pytest.mark.parametrize("B,T,pos", [(2, 9, [300, -1]), (1, 24, [5000])])
+def test_new_outputs_are_zero_where_there_is_no_node(heads, B, T, pos):
+    """A new out holds zeros in the rows of places without a node, whatever its
+    memory held; the other rows are what a given out receives."""
+    m = 4
+    s = attn_case("hca", B, T, pos, "padded", m, 16, 0, seed=6, **heads)
+    live = torch.tensor([[pos[b] >= 0 and R.path_of(s["parents"][b], i) is not None for i in range(T)] for b in range(B)], device=DEV)
+    assert not live.all()
+    want = run_attn(s, out=torch.zeros_like(s["q"]))
+    junk = torch.full((64 << 20,), float("nan"), device=DEV)                # (what the allocator hands out next)
+    del junk
+    got = run_attn(s)
+    assert torch.equal(got, want) and not got[~live].any()
+    dt, c = s["q"].dtype, 128
+    g = gen(7)
+    streams = [torch.randn(B, T, c, generator=g, device=DEV).to(dt) for _ in range(4)]
+    ring = torch.randn(B, 2 * m, 4, c, generator=g, device=DEV).to(dt)
+    bias = [torch.randn(m, c, generator=g, device=DEV) for _ in range(2)]
+    args = ("csa", streams, ring, R.ints(pos, DEV), R.ints(s["parents"], DEV), bias[0], m)
+    for f8 in (False, True) if dt == torch.bfloat16 else (False,):
+        kw = dict(bias_b=bias[1], rope_dims=64, kv_fp8=f8)
+        shape = api.tree_compress(*args, **kw).shape
+        want = api.tree_compress(*args, out=torch.zeros(shape, dtype=torch.uint8 if f8 else dt, device=DEV), **kw)
+        junk = torch.full((4 << 20,), float("nan"), device=DEV)
+        del junk
+        got = api.tree_compress(*args, **kw)
+        assert torch.equal(got, want)
+        for b in range(B):
+            for i in range(T):
+                done = bool(live[b, i]) and (R.node_position(s["parents"][b], pos[b], i) + 1) % m == 0
+                assert done == bool(got[b, i].any())
+    assert api.device_error() == 0
+
+
 def test_wrapper_refusals():
     s = attn_case("csa", 1, 3, [100], "chain", 4, 16, 8, **SMALL)
     for kw, err in ((dict(idx_in=s["idx"].long()), TypeError), (dict(idx_in=s["idx"][:, :2]), ValueError),
