@@ -18,6 +18,7 @@
 #include "decode_compress.cuh"
 #include "indexer_simt.cuh"
 #include "topk.cuh"
+#include "topk_rows_wide.cuh"
 #include "topk_large.cuh"
 #include "attention_simt.cuh"
 #include "indexer_tc.cuh"
@@ -295,6 +296,12 @@ constexpr int kTopkSmallMaxN = kTopkSmemMaxN;   // rows up to this length: one C
 
 bool topk_uses_large(const csahca_indexer_args* a) { return a->N > kTopkSmallMaxN; }
 
+// Few short rows: a CTA of 1,024 threads each, the scores of the selection
+// (sel_scores) in the same pass.
+bool topk_uses_wide(const csahca_indexer_args* a, int64_t rows) {
+  return !topk_uses_large(a) && rows <= num_sms();
+}
+
 // Scratch of the multi-CTA top-k for `rows` rows of length N.
 struct TopkLargeLayout { size_t hist, counters, above, cand, total; };
 TopkLargeLayout topk_large_layout(int64_t rows, int N, int k) {
@@ -343,12 +350,19 @@ int launch_zero(char* ptr, size_t bytes, cudaStream_t s) {
 int launch_topk(const csahca_indexer_args* a, const float* scores, int64_t stride, const int* q_pos, int* idx,
                 int rows, char* scratch, cudaStream_t s, bool hist_ready = false,
                 const void* prefetch_base = nullptr, int64_t prefetch_row_bytes = 0, bool sorted = true,
-                bool routed = false) {
+                bool routed = false, float* sel = nullptr) {
   if (!topk_uses_large(a)) {
     TopkParams tp;
     tp.scores = scores; tp.row_stride = stride; tp.q_pos = q_pos; tp.idx = idx;
     tp.B = 1; tp.nq = rows; tp.N = a->N; tp.m = a->m; tp.k = a->k;
     tp.q_begin = 0; tp.q_count = rows; tp.entry_base = a->entry_base;
+    if (topk_uses_wide(a, rows)) {
+      CSAHCA_TRACE("topk_rows_wide", s);
+      auto kern = a->N <= 4096 ? topk_rows_wide_kernel<4> : a->N <= 16384 ? topk_rows_wide_kernel<16> : topk_rows_wide_kernel<32>;
+      launch_k(kern, dim3(rows), dim3(kTopkWideThreads), 0, s, tp, sel);
+      CSAHCA_CHECK_LAUNCH();
+      return CSAHCA_OK;
+    }
     CSAHCA_TRACE("topk_rows", s);
     launch_k(topk_rows_sample_kernel, dim3(rows), dim3(kTopkStreamThreads), 0, s, tp);
     CSAHCA_CHECK_LAUNCH();
@@ -609,9 +623,10 @@ int run_indexer(const csahca_indexer_args* a, void* stream, const void* prefetch
           CSAHCA_CHECK_LAUNCH();
         }
         int st3 = launch_topk(a, pb.scores, stride, pb.q_pos + q0, a->idx + ((int64_t)b * a->nq + q0) * a->k, qc,
-                              static_cast<char*>(a->workspace), s);
+                              static_cast<char*>(a->workspace), s, false, nullptr, 0, true, false,
+                              a->sel_scores ? a->sel_scores + ((int64_t)b * a->nq + q0) * a->k : nullptr);
         if (st3 != CSAHCA_OK) return st3;
-        if (a->sel_scores) {
+        if (a->sel_scores && !topk_uses_wide(a, qc)) {
           const int64_t r0 = (int64_t)b * a->nq + q0;
           st3 = launch_select_scores(pb.scores, stride, a->idx + r0 * a->k, a->sel_scores + r0 * a->k, qc, a->k, s);
           if (st3 != CSAHCA_OK) return st3;
@@ -668,9 +683,9 @@ int run_indexer(const csahca_indexer_args* a, void* stream, const void* prefetch
     // addressed per batch entry, so launch per b unless the chunk is the whole nq
     if (qc == a->nq) {
       int st3 = launch_topk(a, base, stride, a->q_pos, a->idx, a->B * qc, scratch, s, fuse_hist,
-                            a->nq == 1 ? prefetch_base : nullptr, prefetch_row_bytes, sorted, route);
+                            a->nq == 1 ? prefetch_base : nullptr, prefetch_row_bytes, sorted, route, a->sel_scores);
       if (st3 != CSAHCA_OK) return st3;
-      if (a->sel_scores) {
+      if (a->sel_scores && !topk_uses_wide(a, (int64_t)a->B * qc)) {
         st3 = launch_select_scores(base, stride, a->idx, a->sel_scores, a->B * qc, a->k, s);
         if (st3 != CSAHCA_OK) return st3;
       }
@@ -678,9 +693,10 @@ int run_indexer(const csahca_indexer_args* a, void* stream, const void* prefetch
       for (int b = 0; b < a->B; ++b) {
         const int64_t r0 = (int64_t)b * a->nq + q0;
         int st3 = launch_topk(a, base + (int64_t)b * qc * stride, stride, a->q_pos + (int64_t)b * a->nq + q0,
-                              a->idx + r0 * a->k, qc, scratch, s);
+                              a->idx + r0 * a->k, qc, scratch, s, false, nullptr, 0, true, false,
+                              a->sel_scores ? a->sel_scores + r0 * a->k : nullptr);
         if (st3 != CSAHCA_OK) return st3;
-        if (a->sel_scores) {
+        if (a->sel_scores && !topk_uses_wide(a, qc)) {
           st3 = launch_select_scores(base + (int64_t)b * qc * stride, stride, a->idx + r0 * a->k,
                                      a->sel_scores + r0 * a->k, qc, a->k, s);
           if (st3 != CSAHCA_OK) return st3;
