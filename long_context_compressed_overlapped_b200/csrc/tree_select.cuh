@@ -10,7 +10,10 @@
 // The y that stay push out the y - f lowest candidates (of equal scores the
 // higher index first), found one after another: mostly none or very few.
 //
-// One CTA per node; a node without drafted entries leaves at once.
+// One CTA per node.  The drafted scores need only the call's inputs, which were
+// complete before the kernels of this call began (each of them waits for its
+// predecessor before it lets its successor start): they are formed while the
+// top-k of the committed entries still runs.
 #pragma once
 #include "norm_rope.cuh"
 #include "topk.cuh"
@@ -49,11 +52,14 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   __shared__ float dscore[kTreeMaxNodes], part_s[kTsThreads / 32];
   __shared__ int nd_s, valid_s, scan_s[kTsThreads / 32];
   __shared__ unsigned long long min_s;
-  griddep_wait();
-  griddep_launch_dependents();
   const int node = blockIdx.x, b = node / p.T, i = node - b * p.T;
   const int t = tree_node(p.parents, p.pos, b, p.T, i, &node_s);
-  if (t < 0) return;
+  // (a CTA that leaves waits all the same: the attention behind this kernel reads
+  // what the one before it wrote)
+  if (t < 0) {
+    griddep_wait();
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   if (tid == 0) {
     int nd = 0;
@@ -65,7 +71,10 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   if (tid < kTreeMaxNodes) below[tid] = 0;
   __syncthreads();
   const int nd = nd_s;
-  if (nd == 0) return;
+  if (nd == 0) {
+    griddep_wait();
+    return;
+  }
   // scores of the drafted entries: a warp takes every eighth head
   for (int x = 0; x < nd; ++x) {
     const int64_t krow = (int64_t)b * p.T + dnode[x];
@@ -86,6 +95,8 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
     }
     __syncthreads();
   }
+  griddep_wait();
+  griddep_launch_dependents();
   // descending rank of each drafted entry (ties: the earlier one first)
   if (tid < nd) {
     int r = 0;
