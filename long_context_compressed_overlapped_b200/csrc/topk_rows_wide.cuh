@@ -16,9 +16,9 @@
 //
 // indexer_topk with the selection's scores, 18 queries, k = 1,024, here / with
 // 256 threads a row and the scores read back by another kernel: 4,096 keys
-// 18 / 29 us, 16,384 keys 25 / 54 us, 32,768 keys 37 / 76 us (k = 4,096, where the
-// lists of 256 threads run over: 39 / 192 us); 148 queries of 16,384 keys
-// 55 / 86 us.
+// 18 / 29 us, 16,384 keys 25 / 54 us, 32,768 keys 35 / 76 us (k = 4,096, where the
+// lists of 256 threads run over: 37 / 192 us); 148 queries of 16,384 keys
+// 56 / 86 us.
 #pragma once
 #include "topk.cuh"
 
@@ -72,6 +72,18 @@ __device__ __forceinline__ float topk_wide_score(uint32_t u) {
   return __uint_as_float(u == 1u ? 0x7fffffffu : (u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
+// f(x) for the registers that a row with ranges of L keys fills, eight at a time.
+template <int KPL, typename F> __device__ __forceinline__ void topk_wide_each(int L, F f) {
+  constexpr int G = KPL < 8 ? KPL : 8;
+#pragma unroll
+  for (int g = 0; g < KPL; g += G) {
+    if (32 * g < L) {
+#pragma unroll
+      for (int x = g; x < g + G; ++x) f(x);
+    }
+  }
+}
+
 // KPL: keys a lane holds, at least ceil(N / 1024).  sel (optional): the scores of
 // the selection, -inf behind it.
 template <int KPL>
@@ -95,18 +107,16 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
   const int L = (v + kTopkWideThreads - 1) / kTopkWideThreads * 32;      // <= 32 KPL
   const int j0 = wid * L, j1 = min(v, j0 + L);
   uint32_t u[KPL];                                   // order keys; NaN: 1, no key: 0 (below -inf's)
-#pragma unroll
-  for (int x = 0; x < KPL; ++x) {
+  topk_wide_each<KPL>(L, [&](int x) {
     const int j = j0 + 32 * x + lane;
-    u[x] = j < j1 ? __float_as_uint(__ldg(r.s + j)) : 0x7fffffffu;
-  }
+    u[x] = j < j1 ? __float_as_uint(__ldg(r.s + j)) : 0u;
+  });
   if (threadIdx.x == 0) sm.sampled = sm.listed = 0;
   for (int x = threadIdx.x; x < 2048; x += kTopkWideThreads) sm.hist[x] = 0u;
-#pragma unroll
-  for (int x = 0; x < KPL; ++x) {
+  topk_wide_each<KPL>(L, [&](int x) {
     const float f = __uint_as_float(u[x]);
     u[x] = j0 + 32 * x + lane < j1 ? (f == f ? order_key(f) : 1u) : 0u;
-  }
+  });
   __syncthreads();
 
   // ---- a bound that about 5 k / 4 keys reach
@@ -115,8 +125,10 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
     int n = 0;
 #pragma unroll
     for (int x = 0; x < KPL; x += 8) {
-      if (u[x]) atomicAdd(&sm.hist[u[x] >> 21], 1u);
-      n += __popc(__ballot_sync(0xffffffffu, u[x] != 0u));
+      if (32 * x < L) {
+        if (u[x]) atomicAdd(&sm.hist[u[x] >> 21], 1u);
+        n += __popc(__ballot_sync(0xffffffffu, u[x] != 0u));
+      }
     }
     if (lane == 0 && n) atomicAdd(&sm.sampled, n);
     __syncthreads();
@@ -130,8 +142,7 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
 
   // ---- the keys that reach the bound, in any order, to a list (if it holds them)
   int keep = 0;
-#pragma unroll
-  for (int x = 0; x < KPL; ++x) keep += u[x] >= lo;
+  topk_wide_each<KPL>(L, [&](int x) { keep += u[x] >= lo; });
   int incl = keep;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,9 +152,9 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
   int at = lane == 31 ? atomicAdd(&sm.listed, incl) : 0;
   at = __shfl_sync(0xffffffffu, at, 31) + incl - keep;
   if (at + keep <= kTopkWideList) {
-#pragma unroll
-    for (int x = 0; x < KPL; ++x)
+    topk_wide_each<KPL>(L, [&](int x) {
       if (u[x] >= lo) sm.list[at++] = u[x];
+    });
   }
   __syncthreads();
   const int nl = sm.listed;
@@ -165,9 +176,9 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
     if (listed) {
       for (int x = threadIdx.x; x < nl; x += kTopkWideThreads) count(sm.list[x]);
     } else {
-#pragma unroll
-      for (int x = 0; x < KPL; ++x)
+      topk_wide_each<KPL>(L, [&](int x) {
         if (u[x] >= lo) count(u[x]);
+      });
     }
     __syncthreads();
     topk_wide_digit(sm, nb, need);
@@ -177,11 +188,10 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
 
   // ---- each warp's place in the output, then its keys in index order
   unsigned n_gt = 0, n_eq = 0;
-#pragma unroll
-  for (int x = 0; x < KPL; ++x) {
+  topk_wide_each<KPL>(L, [&](int x) {
     n_gt += u[x] > T;
     n_eq += u[x] == T;
-  }
+  });
   n_gt = __reduce_add_sync(0xffffffffu, n_gt);
   n_eq = __reduce_add_sync(0xffffffffu, n_eq);
   if (lane == 0) { sm.wcnt[wid][0] = (int)n_gt; sm.wcnt[wid][1] = (int)n_eq; }
@@ -203,23 +213,21 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
   };
   if (eq_take == 0 || eq_take == (int)n_eq) {        // no tie is split here
     const uint32_t thr = eq_take == 0 ? T + 1u : T;  // (a key is at most that of +inf)
-#pragma unroll
-    for (int x = 0; x < KPL; ++x) {
+    topk_wide_each<KPL>(L, [&](int x) {
       const uint32_t tb = __ballot_sync(0xffffffffu, u[x] >= thr);
       if (u[x] >= thr) put(x, pos + __popc(tb & lt));
       pos += __popc(tb);
-    }
+    });
   } else {
     int eq_seen = 0;
-#pragma unroll
-    for (int x = 0; x < KPL; ++x) {
+    topk_wide_each<KPL>(L, [&](int x) {
       const uint32_t eqb = __ballot_sync(0xffffffffu, u[x] == T);
       const bool take = u[x] > T || (u[x] == T && eq_seen + __popc(eqb & lt) < eq_take);
       const uint32_t tb = __ballot_sync(0xffffffffu, take);
       if (take) put(x, pos + __popc(tb & lt));
       pos += __popc(tb);
       eq_seen += __popc(eqb);
-    }
+    });
   }
 }
 
