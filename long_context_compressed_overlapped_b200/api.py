@@ -422,17 +422,16 @@ def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=N
     if fresh:
         out = torch.empty(oshape, dtype=odt, device=dev)
     p = [_arg("streams", t, dev, shape, dt) for t in streams]
+    # (in the struct's order)
     a = N.TreeCompressArgs(
-        kind=N.CSA if csa else N.HCA, dtype=code, out_dtype=N.E4M3 if f8 else code, B=B, T=T, c=c, m=m,
-        rms_norm=bool(rms_norm), rope_dims=rope_dims, rope_base=rope_base, eps=eps, kv_rows=bool(kv_fp8),
-        zero_rest=fresh,
-        pos=_ints("pos", pos, dev, (B,), keep), parents=_ints("parents", parents, dev, (B, T), keep),
-        a=p[0], b=p[1] if csa else None, za=p[2 if csa else 1], zb=p[3] if csa else None,
-        ring=_arg("ring", ring, dev, (B, 2 * m, 4, c) if csa else (B, m, 2, c), dt),
-        bias_a=_floats("bias_a", bias_a, dev, (m, c), keep, False),
-        bias_b=_floats("bias_b", bias_b, dev, (m, c), keep, not csa), gain=_floats("gain", gain, dev, (c,), keep),
-        out=_arg("out", out, dev, oshape, odt),
-        out_scale=_arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32, True))
+        N.CSA if csa else N.HCA, code, N.E4M3 if f8 else code, B, T, c, m, bool(rms_norm), rope_dims, rope_base, eps,
+        bool(kv_fp8), fresh, 0, _ints("pos", pos, dev, (B,), keep), _ints("parents", parents, dev, (B, T), keep),
+        p[0], p[1] if csa else None, p[2 if csa else 1], p[3] if csa else None,
+        _arg("ring", ring, dev, (B, 2 * m, 4, c) if csa else (B, m, 2, c), dt),
+        _floats("bias_a", bias_a, dev, (m, c), keep, False),
+        _floats("bias_b", bias_b, dev, (m, c), keep, False) if csa else None,
+        None if gain is None else _floats("gain", gain, dev, (c,), keep), _arg("out", out, dev, oshape, odt),
+        None if out_scale is None else _arg("out_scale", out_scale, dev, (B, T, c // 128), torch.float32))
     return a, out, keep
 
 
