@@ -296,14 +296,29 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _keep_for(stream, x):
+    """Tensors among x (nested): their memory stays theirs until the stream has read it."""
+    if isinstance(x, torch.Tensor):
+        if x.is_cuda:
+            x.record_stream(stream)
+    elif isinstance(x, dict):
+        _keep_for(stream, x.values())
+    elif not isinstance(x, (str, int, float, type(None))):
+        for y in x:
+            _keep_for(stream, y)
+
+
 def _on(stream, dev, call, *args):
     """call(*args) with the tensors' device current and the given stream (or
-    the device's current one) as the stream of its allocations and kernels."""
+    the device's current one) as the stream of its allocations and kernels.
+    On a stream that is not the current one the caller may drop the tensors
+    as soon as the call returns."""
     if dev.type != "cuda":
         raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        _keep_for(stream, args)
         with torch.cuda.stream(stream):
             return call(*args)
     if torch.cuda.current_device() == dev.index:

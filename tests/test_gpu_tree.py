@@ -522,6 +522,43 @@ def test_streams_graphs_and_workspaces(kind):
     assert api.device_error() == 0
 
 
+def test_inputs_live_until_the_stream_has_read_them():
+    """Arguments that the caller drops after a call on another stream: their
+    memory is not handed out again before that stream has read it."""
+    st = torch.cuda.Stream()
+    s = attn_case("hca", 2, 6, [3000, 2999], "wide", 16, 128, 0, **TC)
+    pos, parents = R.ints(s["pos"], DEV), R.ints(s["parents"], DEV)
+    g = gen(9)
+    streams = [torch.randn(2, 6, 512, generator=g, device=DEV).bfloat16() for _ in range(2)]
+    ring, bias = torch.randn(2, 16, 2, 512, generator=g, device=DEV).bfloat16(), torch.randn(16, 512, generator=g, device=DEV)
+    node_pos = torch.arange(12, device=DEV, dtype=torch.int32).view(2, 6) * 100
+
+    def attn(pos, parents, **kw):
+        return api.compressed_attn_tree("hca", s["q"], pos, parents, s["kv"], s["win"], s["kv_raw"], s["sinks"], m=16, rope_dims=64,
+                                        draft=s["draft"], **kw)
+
+    def comp(pos, parents, **kw):
+        return api.tree_compress("hca", streams, ring, pos, parents, bias, 16, rope_dims=64, **kw)
+
+    def norm(pos, parents, **kw):
+        return api.qk_norm_rope(s["q"], None, pos, rope_dims=64, q_out=torch.zeros_like(s["q"]), **kw)[0]
+    slow = torch.randn(4096, 4096, device=DEV)
+    for call, p in ((attn, pos), (comp, pos), (norm, node_pos)):
+        want = call(p, parents)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            for _ in range(10):
+                slow = slow @ slow * 1e-3
+        args = [p.clone(), parents.clone()]
+        torch.cuda.current_stream().synchronize()
+        got = call(*args, stream=st)
+        del args
+        junk = [torch.full_like(x, -1) for x in (p, parents) for _ in range(200)]      # (-1: a sequence, token or node that is left alone)
+        st.synchronize()
+        assert torch.equal(got, want), call.__name__
+        del junk
+
+
 @pytest.mark.parametrize("heads", [SMALL, TC, HEADS16], ids=["f32", "tc", "16h"])
 @pytest.mark.parametrize("B,T,pos", [(2, 9, [300, -1]), (1, 24, [5000])])
 def test_new_outputs_are_zero_where_there_is_no_node(heads, B, T, pos):
