@@ -820,11 +820,15 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
 // One CTA per (node, 32 dims).  The partials are in L2; each thread reads its
 // dim pair's 4 heads of four splits at a time, the first ones together with the
 // headers, so that a few splits cost one round trip (10 us with the position,
-// the maxima, the sums and O read one after another).
+// the maxima, the sums and O read one after another).  Up to 16 splits a head's
+// maxima and sums stay in registers between its sum and the weights; the
+// weights carry 1 / den, once a head and split instead of in every thread (64
+// nodes of two splits: some 1 us less; 64 dims a CTA, one wave instead of two: 0.5 us
+// less again, not worth a second form).
 constexpr int kTreeCombineDims = 32;
 constexpr int kTreeCombineThreads = 256;
 constexpr int kTreeMaxSplits = 148;
-__host__ __device__ constexpr int tree_combine_smem(int splits) { return splits * 2 * kAttnH * 4; }
+__host__ __device__ constexpr int tree_combine_smem(int splits) { return splits * kAttnH * 4; }
 
 struct TreeCombineParams {
   const char* partial; const float* sinks; const int* node_pos;
@@ -833,10 +837,10 @@ struct TreeCombineParams {
   double theta[64];
 };
 
-__global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const __grid_constant__ TreeCombineParams p) {
+__global__ void __launch_bounds__(kTreeCombineThreads, 4) tree_combine_kernel(const __grid_constant__ TreeCombineParams p) {
+  constexpr int U = 4;                                   // splits of a thread in flight
   extern __shared__ __align__(16) float cmb_s[];
   float (*w_s)[kAttnH] = reinterpret_cast<float (*)[kAttnH]>(cmb_s);
-  float (*l_s)[kAttnH] = w_s + p.splits;
   __shared__ __align__(16) __nv_bfloat16 stage[kAttnH][kTreeCombineDims + 8];
   __shared__ float red[4][kAttnH], red2[4][kAttnH];
   griddep_wait();
@@ -845,67 +849,72 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
   const int tid = threadIdx.x;
   const float* P = reinterpret_cast<const float*>(p.partial) + (int64_t)node * p.splits * kTreePartialFloats;
   const int dp = tid >> 4, h4 = (tid & 15) * 4;          // dims d0 + 2 dp, + 1; heads h4 .. h4 + 3
-  const float* src0 = P + tree_partial_at(d0 + 2 * dp, h4);
-  const float* src1 = P + tree_partial_at(d0 + 2 * dp + 1, h4);
   // the position, the headers and the first splits' O are asked for together
   // (the partial blocks of a place without a node hold no numbers, but exist)
   const int t = p.node_pos[node];
   const int h = tid & 63, part = tid >> 6;
   const float z2 = p.sinks[h] * kLog2e;
-  float4 x[4], y[4];
+  float4 x[U], y[U];
+  const auto load = [&](int s0) {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    if (u < p.splits) {
-      x[u] = *reinterpret_cast<const float4*>(src0 + (int64_t)u * kTreePartialFloats);
-      y[u] = *reinterpret_cast<const float4*>(src1 + (int64_t)u * kTreePartialFloats);
-    }
-  }
-  // weights: thread (head h, part) takes the splits part, part + 4, ...
-  float mx = -INFINITY;
-#pragma unroll 4
-  for (int s = part; s < p.splits; s += 4) {
-    const float m = P[(int64_t)s * kTreePartialFloats + h];
-    l_s[s][h] = P[(int64_t)s * kTreePartialFloats + kAttnH + h];
-    w_s[s][h] = m;
-    mx = fmaxf(mx, m);
-  }
-  if (t < 0) return;
-  red[part][h] = mx;
-  __syncthreads();
-  const float mk = fmaxf(fmaxf(red[0][h], red[1][h]), fmaxf(red[2][h], red[3][h]));
-  const float M = fmaxf(mk, z2);
-  float den = 0.f;
-  for (int s = part; s < p.splits; s += 4) {
-    const float m = w_s[s][h];
-    const float f = m == -INFINITY ? 0.f : l_s[s][h] * exp2f(m - M);
-    w_s[s][h] = f;
-    den += f;
-  }
-  red2[part][h] = den;
-  __syncthreads();
-  // each thread's four heads: 1 / den (0: no key, or all weight on an infinite sink)
-  float inv[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int hh = h4 + e;
-    const float ze = p.sinks[hh] * kLog2e;
-    const float mke = fmaxf(fmaxf(red[0][hh], red[1][hh]), fmaxf(red[2][hh], red[3][hh]));
-    const float de = red2[0][hh] + red2[1][hh] + red2[2][hh] + red2[3][hh] + exp2f(ze - fmaxf(mke, ze));
-    inv[e] = (mke == -INFINITY || ze == INFINITY) ? 0.f : 1.f / de;
-  }
-  float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = 0; s0 < p.splits; s0 += 4) {
-    if (s0 > 0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (s0 + u < p.splits) {
-          x[u] = *reinterpret_cast<const float4*>(src0 + (int64_t)(s0 + u) * kTreePartialFloats);
-          y[u] = *reinterpret_cast<const float4*>(src1 + (int64_t)(s0 + u) * kTreePartialFloats);
-        }
+    for (int u = 0; u < U; ++u) {
+      if (s0 + u < p.splits) {
+        const float* src = P + (int64_t)(s0 + u) * kTreePartialFloats;
+        x[u] = *reinterpret_cast<const float4*>(src + tree_partial_at(d0 + 2 * dp, h4));
+        y[u] = *reinterpret_cast<const float4*>(src + tree_partial_at(d0 + 2 * dp + 1, h4));
       }
     }
+  };
+  load(0);
+  // head h: the maximum M and the sum over the splits part, part + 4, ...
+  float M = -INFINITY, den = 0.f, ms[4], ls[4];
+  for (int s0 = part; s0 < p.splits; s0 += 16) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+      const int s = s0 + 4 * u;
+      ms[u] = s < p.splits ? P[(int64_t)s * kTreePartialFloats + h] : -INFINITY;
+      ls[u] = s < p.splits ? P[(int64_t)s * kTreePartialFloats + kAttnH + h] : 0.f;
+    }
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) Mn = fmaxf(Mn, ms[u]);
+    const float Ms = Mn == -INFINITY ? 0.f : Mn;
+    den *= exp2f(M - Ms);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) den = ms[u] == -INFINITY ? den : fmaf(ls[u], exp2f(ms[u] - Ms), den);
+    M = Mn;
+  }
+  if (t < 0) return;
+  red[part][h] = M;
+  red2[part][h] = den;
+  __syncthreads();
+  // the head's over all splits and the sink
+  float Mt = z2;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) Mt = fmaxf(Mt, red[u][h]);
+  const float Ms = Mt == -INFINITY ? 0.f : Mt;
+  den = exp2f(z2 - Ms);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) den = red[u][h] == -INFINITY ? den : fmaf(red2[u][h], exp2f(red[u][h] - Ms), den);
+  // the splits' weights (0: no key, or all weight on an infinite sink)
+  const float inv = z2 == INFINITY ? 0.f : 1.f / den;
+  const auto weight = [&](int s, float m, float l) {
+    w_s[s][h] = m == -INFINITY || z2 == INFINITY ? 0.f : l * exp2f(m - Ms) * inv;
+  };
+  if (p.splits <= 16) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (part + 4 * u < p.splits) weight(part + 4 * u, ms[u], ls[u]);
+  } else {
+    for (int s = part; s < p.splits; s += 4)
+      weight(s, P[(int64_t)s * kTreePartialFloats + h], P[(int64_t)s * kTreePartialFloats + kAttnH + h]);
+  }
+  __syncthreads();
+  float a0[4] = {0.f, 0.f, 0.f, 0.f}, a1[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < p.splits; s0 += U) {
+    if (s0 > 0) load(s0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       if (s0 + u < p.splits) {
         const float4 w = *reinterpret_cast<const float4*>(&w_s[s0 + u][h4]);
         const float ws[4] = {w.x, w.y, w.z, w.w};
@@ -913,14 +922,12 @@ __global__ void __launch_bounds__(kTreeCombineThreads) tree_combine_kernel(const
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           // (a split of weight 0 may hold no O: its bytes are not used)
-          a0[e] += ws[e] > 0.f ? ws[e] * xs[e] : 0.f;
-          a1[e] += ws[e] > 0.f ? ws[e] * ys[e] : 0.f;
+          a0[e] += ws[e] != 0.f ? ws[e] * xs[e] : 0.f;
+          a1[e] += ws[e] != 0.f ? ws[e] * ys[e] : 0.f;
         }
       }
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) { a0[e] = inv[e] != 0.f ? a0[e] * inv[e] : 0.f; a1[e] = inv[e] != 0.f ? a1[e] * inv[e] : 0.f; }
   const int j0 = d0 + 2 * dp - (kAttnD - p.rope_dims);
   if (j0 >= 0) {
     float cs, sn;
