@@ -11,7 +11,8 @@
 // one another: in rows above 4,096 keys a histogram of every eighth 32-key
 // segment first gives a bound, and the some 5 k / 4 keys that reach it go to a
 // list for the histograms (fewer than k of them, or more than the list holds:
-// they count the registers).  The warps then place their keys > T and lowest-index keys == T by ballots, in index order.
+// the registers are counted).  The warps then place their keys > T and
+// lowest-index keys == T by ballots, in index order.
 // A NaN ranks below every score.
 //
 // indexer_topk with the selection's scores, 18 queries, k = 1,024, here / with
