@@ -130,6 +130,16 @@ def test_strides_of_dims_of_size_one():
     check(y, ref, torch.float32, 64, np.ones((1, 1), bool))
 
 
+def test_rows_past_32_bit_offsets():
+    """The last of 2.6e9 elements: the same bits as from a call on them alone."""
+    n, last = 80_000, 50
+    q = torch.randn(1, n, 64, 512, generator=torch.Generator(device=DEV).manual_seed(6), device=DEV, dtype=torch.bfloat16)
+    pos = torch.arange(n, device=DEV, dtype=torch.int32)[None]
+    y, _ = api.qk_norm_rope(q, None, pos, rope_dims=64)
+    z, _ = api.qk_norm_rope(q[:, -last:].contiguous(), None, pos[:, -last:].clone(), rope_dims=64)
+    assert torch.equal(y[:, -last:], z)
+
+
 def test_zero_rows_and_large_rows():
     x = torch.zeros(1, 3, 2, 64, device=DEV)
     x[0, 1] = 1e15

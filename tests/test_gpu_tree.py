@@ -339,6 +339,27 @@ def test_an_entry_named_twice_is_two_keys(heads):
     assert api.device_error() == 0
 
 
+@pytest.mark.parametrize("heads", [64, 5])
+def test_rows_past_32_bit_offsets(heads):
+    """Selected rows at the end of a 6 GB cache: the same bits as from a cache
+    that holds those rows alone."""
+    B, N, tail, T, k = 2, 3_000_000, 5000, 3, 256
+    g = gen(12)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device=DEV).bfloat16()
+    kv = torch.zeros(B, N, 512, device=DEV, dtype=torch.bfloat16)
+    kv[:, -tail:] = normal(B, tail, 512)
+    args = (normal(B, 16, 512), normal(B, T, 512), torch.randn(heads, generator=g, device=DEV))
+    q, draft, parents = normal(B, T, heads, 512), normal(B, T, 512), R.ints([[-1, 0, 1]] * B, DEV)
+    idx = torch.stack([torch.randperm(tail, generator=g, device=DEV)[:k].sort().values for _ in range(B * T)]).view(B, T, k).int()
+    pos = R.ints([4 * N - 1000] * B, DEV)
+    kw = dict(m=4, rope_dims=64, draft=draft)
+    want = api.compressed_attn_tree("csa", q, pos, parents, kv[:, -tail:].contiguous(), *args, idx_in=idx, **kw)
+    got = api.compressed_attn_tree("csa", q, pos, parents, kv, *args, idx_in=idx + (N - tail), **kw)
+    assert torch.equal(got, want) and got.any() and api.device_error() == 0
+
+
 def test_bad_parent_is_reported():
     s = attn_case("hca", 1, 5, [300], "chain", 128, 16, **SMALL)
     s["parents"][0][2] = 2                                                          # its own parent: a walk that must end
