@@ -301,10 +301,8 @@ def _keep_for(stream, x):
     if isinstance(x, torch.Tensor):
         if x.is_cuda:
             x.record_stream(stream)
-    elif isinstance(x, dict):
-        _keep_for(stream, x.values())
-    elif not isinstance(x, (str, int, float, type(None))):
-        for y in x:
+    elif isinstance(x, (tuple, list, dict)):
+        for y in x.values() if isinstance(x, dict) else x:
             _keep_for(stream, y)
 
 
