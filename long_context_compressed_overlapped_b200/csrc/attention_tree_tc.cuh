@@ -69,7 +69,8 @@ struct TreeSmem {
 static_assert(256 * kAttnRegsSoftmax + 32 * kTreeProducers * kAttnRegsProducer + 128 * kAttnRegsMma <= 72 * kTreeThreads,
               "the register split fits a 72-register launch");
 
-// Partial of one (node, split), fp32: m[H], l[H], then O / l as [2 head groups][D]
+// Partial of one (node, split), fp32: m[H], l[H] (l = -1: a split without keys,
+// which has no more than this header), then O / l as [2 head groups][D]
 // rows of 32 heads, 128 bytes each, whose 16-byte piece j holds heads
 // 4 (j ^ (dim & 7)) .. + 3: as the threads write them into shared memory without
 // conflicts, so that a bulk copy takes 16 KB of it at once (stored from the
@@ -714,14 +715,16 @@ attn_tree_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_
         if (p.splits > 1) {
           // m[H] (log2 units), l[H] and O / l [D][H], all fp32 (a node's splits
           // are joined without a rounding in between); a split without keys
-          // writes its header only (m = -inf, l = 0)
+          // writes its header only (m = -inf, l = -1).  NaN among the scores
+          // makes l NaN, which has to reach the join: with no other score of the
+          // head m is still -inf, and 0 in the header
           float* blk = reinterpret_cast<float*>(p.partial + (int64_t)id * kTreePartialBytes);
           if (tid < 32) {
             const int h = h0 + tid;
-            const float l = empty ? 0.f : l_run[h];
-            blk[h] = l > 0.f ? m_run[h] : -INFINITY;
+            const float l = empty ? -1.f : l_run[h], m = empty ? -INFINITY : m_run[h];
+            blk[h] = l != l && m == -INFINITY ? 0.f : m;
             blk[kAttnH + h] = l;
-            stat_a[h] = l > 0.f ? 1.f / l : 0.f;
+            stat_a[h] = l == 0.f ? 0.f : 1.f / l;      // (l = 0: every score was -inf, and O 0 or 0 x inf)
           }
           group_sync(gid);
           if (!empty) {
@@ -896,10 +899,11 @@ __global__ void __launch_bounds__(kTreeCombineThreads, 4) tree_combine_kernel(co
   den = exp2f(z2 - Ms);
 #pragma unroll
   for (int u = 0; u < 4; ++u) den = red[u][h] == -INFINITY ? den : fmaf(red2[u][h], exp2f(red[u][h] - Ms), den);
-  // the splits' weights (0: no key, or all weight on an infinite sink)
+  // the splits' weights (0: every score -inf, or all weight on an infinite sink;
+  // -1: no key, and no O)
   const float inv = z2 == INFINITY ? 0.f : 1.f / den;
   const auto weight = [&](int s, float m, float l) {
-    w_s[s][h] = m == -INFINITY || z2 == INFINITY ? 0.f : l * exp2f(m - Ms) * inv;
+    w_s[s][h] = l < 0.f ? -1.f : m == -INFINITY || z2 == INFINITY ? 0.f : l * exp2f(m - Ms) * inv;
   };
   if (p.splits <= 16) {
 #pragma unroll
@@ -921,9 +925,9 @@ __global__ void __launch_bounds__(kTreeCombineThreads, 4) tree_combine_kernel(co
         const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // (a split of weight 0 may hold no O: its bytes are not used)
-          a0[e] += ws[e] != 0.f ? ws[e] * xs[e] : 0.f;
-          a1[e] += ws[e] != 0.f ? ws[e] * ys[e] : 0.f;
+          // (no O: the bytes are not used)
+          a0[e] += ws[e] < 0.f ? 0.f : ws[e] * xs[e];
+          a1[e] += ws[e] < 0.f ? 0.f : ws[e] * ys[e];
         }
       }
     }
