@@ -1112,7 +1112,7 @@ int run_decode_t(const csahca_decode_args* a, cudaStream_t s, char* ws) {
     c.rows = a->B; c.splits = L.splits; c.rope_dims = a->rope_dims;
     rope_theta_table(c.theta, a->rope_dims, base);              // rope_dims <= 128 on this path
     const int smem = tc_combine_smem_bytes(L.splits);
-    if (smem > 48 * 1024)
+    if (smem > 24 * 1024)                          // (static and dynamic together pass 48 KB only if asked for)
       cudaFuncSetAttribute(attn_combine_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     // the partials as [B * splits blocks][516 rows][64 bf16]: one box takes
     // the m, l headers of every split of a query, one the 16-dim slices
