@@ -141,9 +141,11 @@ __global__ void __launch_bounds__(32 * kSimtHG) attn_simt_kernel(SimtAttnParams 
       }
       const float cmax = warp_max(s);
       const float mnew = fmaxf(mx, cmax);
-      if (mnew != -INFINITY) {
-        const float pr = (s == -INFINITY) ? 0.f : expf(s - mnew);
-        const float corr = (mx == -INFINITY) ? 0.f : expf(mx - mnew);
+      // (a tile of NaN scores has no maximum, but its weights are NaN)
+      if (mnew != -INFINITY || __any_sync(0xffffffffu, s != s)) {
+        const float ms = mnew == -INFINITY ? 0.f : mnew;
+        const float pr = (s == -INFINITY) ? 0.f : expf(s - ms);
+        const float corr = (mx == -INFINITY) ? 0.f : expf(mx - ms);
         lsum = lsum * corr + warp_sum(pr);
 #pragma unroll
         for (int e = 0; e < kSimtMaxDPL; ++e) acc[e] *= corr;

@@ -55,6 +55,10 @@ constexpr int kAttnChunks = kAttnD / 64;
 constexpr int kAttnMT = kAttnD / 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+// Running maximum of a head without a score yet.  Finite, so that a score of
+// -inf (an infinite key) less it is -inf, weight 0, and not NaN; scores below it
+// weigh nothing beside any sink.
+constexpr float kNoMax = -3.0e38f;
 
 struct AttnTcParams {
   const __nv_bfloat16* q; const float* q_gain; const float* sinks; const int* pos;
@@ -715,7 +719,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_const
           rope_cs[st] = cs;
           rope_sn[st] = sn;
         }
-        if (st < kAttnH) m_use[st] = -INFINITY;
+        if (st < kAttnH) m_use[st] = kNoMax;
         // (the 256-thread reduction also publishes rope_cs / rope_sn)
         bad = !softmax_all256(mbar_wait(&bar_q_raw, qcount & 1, &abort_flag));
         ++qcount;
@@ -887,8 +891,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_const
             const int h = h0 + tid;
             const float mt = stat_a[h], mo = m_use[h];
             float a = 1.f;
-            if (mt > mo + kRescaleThreshold || (mo == -INFINITY && mt != -INFINITY)) {
-              a = (mo == -INFINITY) ? 0.f : exp2f(mo - mt);
+            if (mt > mo + kRescaleThreshold) {
+              a = exp2f(mo - mt);                          // (0 from kNoMax)
               m_use[h] = mt;
               if (!first) need_rescale[g] = 1;
             }
@@ -970,14 +974,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_const
           // partial block of (query, split): m[H] (log2 units) and l[H] in
           // fp32, then O / l as bf16 [D][H] (a thread writes its dim's 32
           // heads, 64 contiguous bytes, straight from TMEM); an empty split
-          // writes only its header, m = -inf, which the combine skips
+          // writes only its header, m = -inf, which the combine skips.  So does one
+          // whose scores are all -inf; one whose scores are all NaN has no maximum
+          // either, but its sum has to reach the combine: m = 0
           char* P = reinterpret_cast<char*>(p.partial) +
                     (((int64_t)it.b * p.nq + it.qi) * p.splits + it.split) * kTcPartialBytes;
           float* hdr = reinterpret_cast<float*>(P);
           if (tid < 32) {
             const int h = h0 + tid;
             const float l = empty ? 0.f : l_run[h];
-            hdr[h] = empty ? -INFINITY : m_use[h];
+            const float m = empty ? kNoMax : m_use[h];
+            hdr[h] = m != kNoMax ? m : l != l ? 0.f : -INFINITY;
             hdr[kAttnH + h] = l;
             stat_a[h] = l > 0.f ? 1.f / l : 0.f;
           }
@@ -1035,8 +1042,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap comp_rows, const __grid_const
               const float z2 = p.sinks[h] * kLog2e;
               const float mu = m_use[h];
               const float M = fmaxf(mu, z2);
-              const float den = exp2f(z2 - M) + (mu == -INFINITY ? 0.f : l_run[h] * exp2f(mu - M));
-              stat_a[h] = (mu == -INFINITY) ? 0.f : exp2f(mu - M) / den;   // factor on O
+              const float den = exp2f(z2 - M) + (mu == kNoMax ? 0.f : l_run[h] * exp2f(mu - M));
+              stat_a[h] = (mu == kNoMax) ? 0.f : exp2f(mu - M) / den;   // factor on O
             }
             group_sync(gid);
             __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sP) + g * 32 * 128;   // [32 heads][128 dims]
