@@ -1,7 +1,7 @@
 // Per-query top-k over indexer scores ("Paper Breakdown: DeepSeek-V4",
 // section 4, DSA on Compressed KV: the top-k entries by I_{t,s}).
 //
-// Radix select on order-preserving 32-bit keys gives the exact key T of the
+// Radix select on order-preserving 32-bit keys (NaN last) gives the exact key T of the
 // k-th largest score and how many keys equal to T are taken; a pass in index
 // order then takes every key > T and the lowest-index keys == T (ties to the
 // lower index), placed by prefix counts, so the output comes out sorted
@@ -16,10 +16,13 @@ namespace csahca {
 constexpr int kTopkSmemMaxN = 32768;        // rows up to this length: topk_rows_sample_kernel
                                             // (16-bit candidate indices)
 
+// The order of scores as unsigned keys: -0 and +0 are one value, and a NaN
+// (whatever its bits) ranks below every score.  No score has key 0.
+constexpr uint32_t kOrderKeyNan = 1u;
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f == 0.0f) f = 0.0f;                    // -0 and +0 are one value
-  uint32_t u = __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(f + 0.0f);       // (-0 + 0 = +0)
+  const uint32_t key = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  return f == f ? key : kOrderKeyNan;
 }
 
 // Exclusive block prefix sum of per-thread counts (blockDim.x a multiple of
@@ -357,7 +360,8 @@ __global__ void __launch_bounds__(kTopkStreamThreads) topk_rows_sample_kernel(To
   // at least the score fb whose order key that is (order keys are monotone in
   // the score), so the walk compares scores and forms order keys for kept
   // keys only
-  // (bins below 4 hold no finite score: every key is kept from there)
+  // (bins below 4 hold no finite score: every key but the NaN is kept from
+  // there; where those are needed, the lists hold fewer than k)
   const uint32_t klo = Blo << 21;
   const float fb = Blo < 4 ? -INFINITY : __uint_as_float((klo & 0x80000000u) ? (klo & 0x7fffffffu) : ~klo);
   uint32_t* lk = ck + wid * kTopkSampPerWarp;

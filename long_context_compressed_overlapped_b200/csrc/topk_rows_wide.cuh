@@ -13,7 +13,6 @@
 // list for the histograms (fewer than k of them, or more than the list holds:
 // the registers are counted).  The warps then place their keys > T and
 // lowest-index keys == T by ballots, in index order.
-// A NaN ranks below every score.
 //
 // indexer_topk with the selection's scores, 18 queries, k = 1,024, here / with
 // 256 threads a row and the scores read back by another kernel: 4,096 keys
@@ -68,9 +67,9 @@ __device__ __forceinline__ void topk_wide_digit(TopkWideSmem& sm, int nb, uint32
   __syncthreads();
 }
 
-// The score of an order key (zero's sign is lost); key 1: NaN.
+// The score of an order key (zero's sign is lost).
 __device__ __forceinline__ float topk_wide_score(uint32_t u) {
-  return __uint_as_float(u == 1u ? 0x7fffffffu : (u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+  return __uint_as_float(u == kOrderKeyNan ? 0x7fffffffu : (u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
 }
 
 // f(x) for the registers that a row with ranges of L keys fills, eight at a time.
@@ -107,17 +106,14 @@ __global__ void __launch_bounds__(kTopkWideThreads, 1) topk_rows_wide_kernel(Top
   const uint32_t lt = (1u << lane) - 1u, k = (uint32_t)p.k;
   const int L = (v + kTopkWideThreads - 1) / kTopkWideThreads * 32;      // <= 32 KPL
   const int j0 = wid * L, j1 = min(v, j0 + L);
-  uint32_t u[KPL];                                   // order keys; NaN: 1, no key: 0 (below -inf's)
+  uint32_t u[KPL];                                   // order keys; no key: 0
   topk_wide_each<KPL>(L, [&](int x) {
     const int j = j0 + 32 * x + lane;
     u[x] = j < j1 ? __float_as_uint(__ldg(r.s + j)) : 0u;
   });
   if (threadIdx.x == 0) sm.sampled = sm.listed = 0;
   for (int x = threadIdx.x; x < 2048; x += kTopkWideThreads) sm.hist[x] = 0u;
-  topk_wide_each<KPL>(L, [&](int x) {
-    const float f = __uint_as_float(u[x]);
-    u[x] = j0 + 32 * x + lane < j1 ? (f == f ? order_key(f) : 1u) : 0u;
-  });
+  topk_wide_each<KPL>(L, [&](int x) { u[x] = j0 + 32 * x + lane < j1 ? order_key(__uint_as_float(u[x])) : 0u; });
   __syncthreads();
 
   // ---- a bound that about 5 k / 4 keys reach
