@@ -5,6 +5,8 @@
 // scores.  A node also sees the entries that its own path completes, so its
 // selection is the top k of both: a drafted entry stays if it beats one of the
 // candidates that must then go (ties to the lower index: the committed one).
+// Scores are compared as order keys throughout, as in the top-k, so that a NaN
+// ranks last on either side.
 // With f free places and the node's drafted scores in descending order, the
 // r-th (from 0) stays iff f plus the number of candidates below it exceeds r.
 // The y that stay push out the y - f lowest candidates (of equal scores the
@@ -46,10 +48,11 @@ __device__ __forceinline__ float ts_k(const TreeSelectParams& p, int64_t row, in
 __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_constant__ TreeSelectParams p) {
   extern __shared__ __align__(16) uint8_t ts_smem[];
   int* idx_s = reinterpret_cast<int*>(ts_smem);                   // [k], -1 once pushed out
-  float* sc_s = reinterpret_cast<float*>(idx_s + p.k);            // [k]
+  uint32_t* key_s = reinterpret_cast<uint32_t*>(idx_s + p.k);     // [k] order keys of the scores
   __shared__ TreeNode node_s;
   __shared__ int dnode[kTreeMaxNodes], rank_s[kTreeMaxNodes], below[kTreeMaxNodes];
-  __shared__ float dscore[kTreeMaxNodes], part_s[kTsThreads / 32];
+  __shared__ uint32_t dkey[kTreeMaxNodes];
+  __shared__ float part_s[kTsThreads / 32];
   __shared__ int nd_s, valid_s, scan_s[kTsThreads / 32];
   __shared__ unsigned long long min_s;
   const int node = blockIdx.x, b = node / p.T, i = node - b * p.T;
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
     if (tid == 0) {
       float s = 0.f;
       for (int k = 0; k < kTsThreads / 32; ++k) s += part_s[k];
-      dscore[x] = s == s ? s : -INFINITY;            // (NaN: last, so that the ranks stay distinct)
+      dkey[x] = order_key(s);
     }
     __syncthreads();
   }
@@ -100,21 +103,21 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
   // descending rank of each drafted entry (ties: the earlier one first)
   if (tid < nd) {
     int r = 0;
-    for (int x = 0; x < nd; ++x) r += dscore[x] > dscore[tid] || (dscore[x] == dscore[tid] && x < tid);
+    for (int x = 0; x < nd; ++x) r += dkey[x] > dkey[tid] || (dkey[x] == dkey[tid] && x < tid);
     rank_s[tid] = r;
   }
   int mine = 0;
   for (int j = tid; j < p.k; j += kTsThreads) {
     const int e = p.idx[(int64_t)node * p.k + j];
     idx_s[j] = e;
-    sc_s[j] = e >= 0 ? p.scores[(int64_t)node * p.k + j] : 0.f;
+    key_s[j] = e >= 0 ? order_key(p.scores[(int64_t)node * p.k + j]) : 0u;
     mine += e >= 0;
   }
   if (mine) atomicAdd(&valid_s, mine);
   __syncthreads();
   for (int x = 0; x < nd; ++x) {
     int c = 0;
-    for (int j = tid; j < p.k; j += kTsThreads) c += idx_s[j] >= 0 && sc_s[j] < dscore[x];
+    for (int j = tid; j < p.k; j += kTsThreads) c += idx_s[j] >= 0 && key_s[j] < dkey[x];
     c = (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
     if (lane == 0 && c) atomicAdd(&below[x], c);
   }
@@ -129,8 +132,7 @@ __global__ void __launch_bounds__(kTsThreads) tree_select_kernel(const __grid_co
     int at = -1;
     for (int j = tid; j < p.k; j += kTsThreads) {
       if (idx_s[j] < 0) continue;
-      const unsigned long long key =
-          ((unsigned long long)order_key(sc_s[j]) << 32) | (0xFFFFFFFFu - (uint32_t)idx_s[j]);
+      const unsigned long long key = ((unsigned long long)key_s[j] << 32) | (0xFFFFFFFFu - (uint32_t)idx_s[j]);
       if (key < mn) { mn = key; at = j; }
     }
     if (tid == 0) min_s = ~0ull;
