@@ -496,8 +496,9 @@ int cp_attn_merge(const csahca_cp_merge_args* args, void* stream);
  *   q_out [B, n, HQ, d], k_out [B, n, HK, d] contiguous (either may be its own
  *   input where that is contiguous; else they overlap no input and not each
  *   other).  HQ or HK = 0: that side is left out.
- *   The rows of a token with pos < 0 (padding) are left as they were.
- * Constraints: dtype F32 (d % 4 == 0, d <= 512) or BF16 (d % 8 == 0, d <=
+ *   The rows of a token with pos < 0 (padding) are left as they were, or written
+ *   as zeros where zero_rest says so (bit 0: in q_out, bit 1: in k_out).
+ * Constraints: B * n < 2^31, HQ + HK <= 65535; dtype F32 (d % 4 == 0, d <= 512) or BF16 (d % 8 == 0, d <=
  *   1024); rope_dims even, <= d and <= 512, (d - rope_dims) even.  No
  *   workspace. */
 typedef struct {
@@ -507,7 +508,7 @@ typedef struct {
   float rope_base;     /* 0 -> 10000 */
   float eps;           /* 0 -> 1e-6 */
   int32_t q_norm, k_norm;
-  int32_t reserved0;
+  int32_t zero_rest;   /* 1: padding rows of q_out become zeros, 2: of k_out, 3: of both */
   int64_t q_stride[3];
   int64_t k_stride[3];
   const void* q;

@@ -361,7 +361,7 @@ def _floats(name, t, dev, shape, keep, optional=True):
 
 
 def _heads(name, t, out, gain, dev, dt, B, n, d, keep):
-    """One side of qk_norm_rope: (heads, strides or None, pointers of rows, output and gain, output)."""
+    """One side of qk_norm_rope: (heads, strides or None, pointers of rows, output and gain, output, output is new)."""
     shape = t.shape
     if t.dtype is not dt or t.device != dev or len(shape) != 4 or shape[0] != B or shape[1] != n or shape[3] != d:
         raise ValueError(f"{name}: {tuple(shape)} {t.dtype} on {t.device} does not match the other rows")
@@ -373,12 +373,13 @@ def _heads(name, t, out, gain, dev, dt, B, n, d, keep):
         if not any(strides[:3]):                 # one row for every head (the library's mark of contiguous rows)
             t, strides = t.contiguous(), None
             keep.append(t)
-    if out is None:
+    fresh = out is None
+    if fresh:
         out = torch.empty_like(t, memory_format=torch.contiguous_format)
         o = out.data_ptr()
     else:
         o = _arg(name + "_out", out, dev, shape, dt)
-    return shape[2], strides, t.data_ptr(), o, _floats(name + "_gain", gain, dev, (d,), keep), out
+    return shape[2], strides, t.data_ptr(), o, _floats(name + "_gain", gain, dev, (d,), keep), out, fresh
 
 
 def _norm_rope(q, k, pos, rope_dims, q_gain, k_gain, q_norm, k_norm, rope_base, eps, q_out, k_out):
@@ -388,11 +389,13 @@ def _norm_rope(q, k, pos, rope_dims, q_gain, k_gain, q_norm, k_norm, rope_base, 
     a = N.NormRopeArgs(_dt(x), B, n, 0, 0, d, rope_dims, rope_base, eps, bool(q_norm), bool(k_norm))
     a.pos = _ints("pos", pos, dev, (B, n), keep)
     if q is not None:
-        a.HQ, st, a.q, a.q_out, a.q_gain, q_out = _heads("q", q, q_out, q_gain, dev, dt, B, n, d, keep)
+        a.HQ, st, a.q, a.q_out, a.q_gain, q_out, fresh = _heads("q", q, q_out, q_gain, dev, dt, B, n, d, keep)
+        a.zero_rest = int(fresh)
         if st is not None:
             a.q_stride[:] = st[:3]
     if k is not None:
-        a.HK, st, a.k, a.k_out, a.k_gain, k_out = _heads("k", k, k_out, k_gain, dev, dt, B, n, d, keep)
+        a.HK, st, a.k, a.k_out, a.k_gain, k_out, fresh = _heads("k", k, k_out, k_gain, dev, dt, B, n, d, keep)
+        a.zero_rest |= 2 * fresh
         if st is not None:
             a.k_stride[:] = st[:3]
     N.check(N.lib().qk_norm_rope(C.byref(a), _raw_stream(dev.index)), "qk_norm_rope")
@@ -406,9 +409,11 @@ def qk_norm_rope(q, k, pos, *, rope_dims, q_gain=None, k_gain=None, q_norm=True,
 
     q [B, n, HQ, d] and k [B, n, HK, d] (either may be None): the dims of a head
     contiguous, the other strides free (multiples of 16 bytes), so heads may be
-    slices of one projection; pos [B, n] int32, negative for padding (the rows
-    of such a token are left as they were).  q_out / k_out: contiguous, by
-    default new; a contiguous input may be its own output.  Returns (q_out, k_out)."""
+    slices of one projection; pos [B, n] int32 (at an address that is a
+    multiple of 16, as every argument), negative for padding (the rows of such a
+    token are left as they were, zero in a new output).  q_out / k_out:
+    contiguous, by default new; a contiguous input may be its own output.
+    Returns (q_out, k_out)."""
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k is required")

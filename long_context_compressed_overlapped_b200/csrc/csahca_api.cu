@@ -1369,6 +1369,7 @@ int run_norm_rope(const csahca_norm_rope_args* a, void* stream) {
   p.y[0] = a->q_out; p.y[1] = a->k_out;
   p.gain[0] = a->q_gain; p.gain[1] = a->k_gain;
   p.norm[0] = a->q_norm; p.norm[1] = a->k_norm;
+  p.zero_rest = a->zero_rest;
   const int64_t* st[2] = {a->q_stride, a->k_stride};
   bool any = false;
   for (int k = 0; k < 2; ++k) {

@@ -55,6 +55,7 @@ struct NormRopeParams {
   const float* gain[2];
   int64_t xs[2][3], ys[2][3];           // element strides of batch, token, head
   int heads[2], norm[2];
+  int zero_rest;                        // bit k: rows of y[k] of a token with pos < 0 become zeros
   const int* pos;                       // [B, n]; < 0: the token's rows are left as they are
   int tokens, n, d, rope_dims;
   int tpc, rows_per_cta;                // tokens of a CTA; rows of its token (tpc = 1) that it takes
@@ -167,6 +168,25 @@ template <> __device__ __forceinline__ uint4 f2_store<__nv_bfloat16>(const uint6
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Rows [row_begin, row_end) of a CTA's padding tokens as zeros, a warp a row.
+template <typename T>
+__device__ __forceinline__ void zero_padding(const NormRopeParams& p, const int* pos_s, const int64_t (*off_s)[kNrMaxTokens],
+                                             int tok0, int row_begin, int row_end) {
+  constexpr int VEC = Vec16<T>::N;
+#pragma unroll 1
+  for (int q = 0; q < p.tpc; ++q) {
+    if (tok0 + q >= p.tokens || pos_s[q] >= 0) continue;
+#pragma unroll 1
+    for (int r = row_begin + (threadIdx.x >> 5); r < row_end; r += kNrThreads / 32) {
+      const int k = r >= p.heads[0];
+      if (!(p.zero_rest >> k & 1)) continue;
+      T* y = static_cast<T*>(p.y[k]) + (off_s[2 + k][q] + (r - k * p.heads[0]) * p.d);
+#pragma unroll 1
+      for (int c = threadIdx.x & 31; c < p.d / VEC; c += 32) *reinterpret_cast<uint4*>(y + c * VEC) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+}
+
 // kFull: every lane's NCH pieces exist (d = LPR * NCH * VEC).
 template <typename T, int LPR, int NCH, bool kFull, bool kTree>
 __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
@@ -225,6 +245,7 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
     tk += step_t;
     if (p.tpc > 1 && row >= heads) { row -= heads; ++tk; }
   };
+  bool padding = false;                               // (this thread's token, then any of the CTA's) becomes zeros
   // a node's rows are asked for before its place in the tree is known
   if constexpr (kTree) {
 #pragma unroll
@@ -270,16 +291,25 @@ __global__ void __launch_bounds__(kNrThreads, NCH >= 4 ? 2 : NCH == 2 ? 3 : 4) n
     }
     if (threadIdx.x == 0) pos_s[0] = t;
   } else {
-    if (threadIdx.x < p.tpc) pos_s[threadIdx.x] = tok0 + threadIdx.x < p.tokens ? p.pos[tok0 + threadIdx.x] : -1;
+    if (threadIdx.x < p.tpc) {
+      const bool in = tok0 + threadIdx.x < p.tokens;
+      const int t = in ? p.pos[tok0 + threadIdx.x] : -1;
+      pos_s[threadIdx.x] = t;
+      padding = in && t < 0 && p.zero_rest;
+    }
   }
   if (threadIdx.x < 4 * p.tpc) {
     const int w = threadIdx.x & 3, q = threadIdx.x >> 2, tok = tok0 + q, b = tok / p.n, i = tok - b * p.n;
     const int64_t* st = w < 2 ? p.xs[w] : p.ys[w - 2];
     off_s[w][q] = b * st[0] + i * st[1];
   }
-  __syncthreads();
+  // (one vote: a test of the flag alone moved the compiler's schedule of the
+  // main loop, 409 against 405 us for 16,384 x 65 rows of 512)
+  if constexpr (kTree) __syncthreads();
+  else padding = __syncthreads_or(padding);
 
   if constexpr (!kTree) {
+    if (padding) zero_padding<T>(p, pos_s, off_s, tok0, row_begin, row_end);
 #pragma unroll
     for (int u = 0; u < U; ++u) load_row(u, u * RPC);
   }

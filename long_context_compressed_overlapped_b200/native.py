@@ -95,7 +95,7 @@ class CpMergeArgs(C.Structure):
 class NormRopeArgs(C.Structure):
     _fields_ = [("dtype", i32), ("B", i32), ("n", i32), ("HQ", i32), ("HK", i32), ("d", i32),
                 ("rope_dims", i32), ("rope_base", f32), ("eps", f32), ("q_norm", i32),
-                ("k_norm", i32), ("reserved0", i32), ("q_stride", i64 * 3), ("k_stride", i64 * 3),
+                ("k_norm", i32), ("zero_rest", i32), ("q_stride", i64 * 3), ("k_stride", i64 * 3),
                 ("q", vp), ("k", vp), ("q_gain", vp), ("k_gain", vp), ("pos", vp), ("q_out", vp),
                 ("k_out", vp)]
 
