@@ -186,9 +186,16 @@ class TreeStep:
     tokens into them.  Argument structs and workspaces are built once (one
     workspace for all layers, which follow one another on the stream), so a
     call only enqueues the library's kernels on `stream`; it can be captured
-    into a CUDA graph after it has run once."""
+    into a CUDA graph after it has run once.  A call reads the layers' own
+    tensors: those that change from step to step and would be converted (pos,
+    parents: int32; tw, kI_scale: fp32; contiguous) are refused in other forms."""
 
     def __init__(self, wl: synth.Workload, layers, stream: torch.cuda.Stream, keep_idx: bool = False):
+        for L in layers:
+            for n, dt in (("pos", torch.int32), ("parents", torch.int32), ("tw", torch.float32), ("kI_scale", torch.float32)):
+                t = L.get(n)
+                if t is not None and (t.dtype is not dt or not t.is_contiguous()):
+                    raise TypeError(f"{n}: a contiguous {dt} tensor is expected (the step would read a copy that does not follow it)")
         self.lib = native.lib()
         self.wl, self.layers, self.stream = wl, layers, stream
         stream.wait_stream(torch.cuda.current_stream(stream.device))
