@@ -240,24 +240,32 @@ class TreeStep:
 
     def commit(self, paths: torch.Tensor) -> None:
         """Take the accepted tokens into every layer's compressors, caches and
-        window: paths [B, n] holds each sequence's accepted nodes from the first
-        drafted token down, -1 behind the last.  One decode_compress a depth and
+        window: paths [B, n] (integers) holds each sequence's accepted nodes from
+        the first drafted token down, -1 behind the last; the first number that is
+        no node's (< 0, or >= T) ends the path.  One decode_compress a depth and
         layer; L["pos"] moves on by the accepted tokens.  Runs on the step's
         stream, behind what the current one (which made `paths`) holds; sequences
         without committed tokens to follow (pos < 0) stay as they are."""
+        B, T = self.layers[0]["tq"].shape[:2] if self.layers else (0, 0)
+        if paths.dim() != 2 or paths.shape[0] != B or paths.dtype.is_floating_point:
+            raise ValueError(f"paths: integers [{B}, n] expected, got {paths.dtype} {tuple(paths.shape)}")
+        if T == 0:
+            return
         self.stream.wait_stream(torch.cuda.current_stream(self.stream.device))
         with torch.cuda.stream(self.stream):
             if paths.is_cuda:
                 paths.record_stream(self.stream)
             paths = paths.to(self.stream.device, torch.int64)
+            live = ((paths >= 0) & (paths < T)).cumprod(1).bool()
+            paths = paths.clamp(0, T - 1)
             for L in self.layers:
                 csa = L["kind"] == "csa"
                 for j in range(paths.shape[1]):
                     node = paths[:, j]
-                    pos = torch.where((node >= 0) & (L["pos"] >= 0), L["pos"] + j, -1)
+                    pos = torch.where(live[:, j] & (L["pos"] >= 0), L["pos"] + j, -1)
 
                     def take(x):
-                        return x[torch.arange(x.shape[0], device=x.device), node.clamp(min=0)].contiguous()
+                        return x[torch.arange(x.shape[0], device=x.device), node].contiguous()
                     kw = {}
                     if csa:
                         kw = dict(istreams=tuple(take(x) for x in L["tis"]), ibias_a=L["ibias_a"], ibias_b=L["ibias_b"],
@@ -266,7 +274,7 @@ class TreeStep:
                                         bias_a=L["bias_a"], bias_b=L["bias_b"], kv_raw=take(L["tkv_raw"]), win=L["win"],
                                         kv_gain=L["kv_gain"], rope_dims=self.wl.r, stream=self.stream, **kw)
             for L in self.layers:
-                L["pos"] += ((paths >= 0).sum(1) * (L["pos"] >= 0)).to(L["pos"].dtype)
+                L["pos"] += (live.sum(1) * (L["pos"] >= 0)).to(L["pos"].dtype)
 
 
 class HostIOGraph:
