@@ -243,7 +243,8 @@ class TreeStep:
         window: paths [B, n] (integers) holds each sequence's accepted nodes from
         the first drafted token down, -1 behind the last; the first number that is
         no node's (< 0, or >= T) ends the path.  One decode_compress a depth and
-        layer; L["pos"] moves on by the accepted tokens.  Runs on the step's
+        layer; L["pos"] moves on by the accepted tokens (once, where layers share
+        one tensor).  Runs on the step's
         stream, behind what the current one (which made `paths`) holds; sequences
         without committed tokens to follow (pos < 0) stay as they are."""
         B, T = self.layers[0]["tq"].shape[:2] if self.layers else (0, 0)
@@ -273,8 +274,8 @@ class TreeStep:
                     api.decode_compress(L["kind"], pos, tuple(take(x) for x in L["ts"]), L["ring"], L["kv"], m=L["m"],
                                         bias_a=L["bias_a"], bias_b=L["bias_b"], kv_raw=take(L["tkv_raw"]), win=L["win"],
                                         kv_gain=L["kv_gain"], rope_dims=self.wl.r, stream=self.stream, **kw)
-            for L in self.layers:
-                L["pos"] += (live.sum(1) * (L["pos"] >= 0)).to(L["pos"].dtype)
+            for p in {L["pos"].data_ptr(): L["pos"] for L in self.layers}.values():
+                p += (live.sum(1) * (p >= 0)).to(p.dtype)
 
 
 class HostIOGraph:

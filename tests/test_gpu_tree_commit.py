@@ -1,5 +1,6 @@
 """TreeStep.commit: numbers in a path that are no node's end it (nothing is read
-past the drafted tokens). The state is the decode steps', bit for bit."""
+past the drafted tokens), and layers that share one pos tensor move it once.
+The state is the decode steps', bit for bit."""
 
 import pytest
 import torch
@@ -44,6 +45,17 @@ def test_numbers_that_are_no_nodes_end_a_path(cpu, dtype):
     step.stream.synchronize()
     check_state(wl, layers, before, [full[0][:1], full[1][:2], []], 509)
     assert api.device_error() == 0
+
+
+def test_layers_that_share_their_positions():
+    wl, layers, before, full = make()
+    for L in layers[1:]:
+        L["pos"] = layers[0]["pos"]
+    step = runtime.TreeStep(wl, layers, torch.cuda.Stream())
+    n = max(map(len, full))
+    step.commit(R.ints([p + [-1] * (n - len(p)) for p in full], DEV))
+    step.stream.synchronize()
+    check_state(wl, layers, before, full, 509)
 
 
 def test_paths_of_other_shapes_or_types_are_refused():
