@@ -440,6 +440,7 @@ def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=N
     if fresh:
         out = torch.empty(oshape, dtype=odt, device=dev)
     p = [_arg("streams", t, dev, shape, dt) for t in streams]
+    keep.append((streams, ring, pos, parents, bias_a, bias_b, gain, out, out_scale))
     # (in the struct's order)
     a = N.TreeCompressArgs(
         N.CSA if csa else N.HCA, code, N.E4M3 if f8 else code, B, T, c, m, bool(rms_norm), rope_dims, rope_base, eps,
@@ -497,6 +498,8 @@ def tree_attn_args(kind, q, pos, parents, kv_cache, win, kv_raw, sinks, *, m, ro
     # a uint8 cache holds FP8 KV rows, and so do the drafted entries
     f8 = kv_cache.dtype is torch.uint8
     cdt, cd = (torch.uint8, N.lib().csahca_kv_row_bytes(N.E4M3, d, rope_dims)) if f8 else (dt, d)
+    keep.append((q, pos, parents, kv_cache, win, kv_raw, sinks, draft, qI, wI, kI, kI_scale, draft_kI, draft_kI_scale, idx_in,
+                 idx_out, q_gain, kv_gain, out))
     # (in the struct's order)
     a = N.TreeAttnArgs(
         N.CSA if csa else N.HCA, code, B, T, H, d, Nc, m, w, k, rope_dims, rope_base, eps, scale, bool(q_norm),
