@@ -121,8 +121,9 @@ int hca_compress(const csahca_compress_args* args, void* stream);
  *   I_{t,i} = sum_j w[b,q,j] * max(0, qI[b,q,j,:] . kI[b,i,:])  for the
  *   visible entries i < v = min(N, (t+1)/m);  kI row i = decode(codes) * scale
  *   per 128-element block when k_dtype = E4M3.
- *   idx[b,q,:] = the k entries with the largest I (ties to the lower index),
- *   sorted ascending, padded with -1 when v < k.
+ *   idx[b,q,:] = the k entries with the largest I (ties to the lower index; a
+ *   NaN ranks below every other score), sorted ascending, padded with -1 when
+ *   v < k.
  * Layout: qI [B, nq, HI, dI] (q_dtype F32/BF16); w [B, nq, HI] f32;
  *   kI [B, N, dI] (k_dtype F32/BF16/E4M3); kI_scale [B, N, dI/128] f32 (E4M3
  *   only, else NULL); q_pos [B, nq] int32 on the device; idx [B, nq, k] int32.
@@ -600,7 +601,7 @@ int tree_compress(const csahca_tree_compress_args* args, void* stream);
  *   indexer selects the k best of the pos[b] / m committed entries (qI [B, T, HI,
  *   dI], wI [B, T, HI] f32, kI and kI_scale as in compressed_attn_decode) and,
  *   where draft_kI is given, of the entries that the node's path completes, by
- *   score, ties to the lower index.  draft_kI [B, T, dI] (kI_dtype; E4M3 with
+ *   score as in indexer_topk, ties to the lower index.  draft_kI [B, T, dI] (kI_dtype; E4M3 with
  *   draft_kI_scale [B, T, dI / 128]) are the drafted entries' indexer keys
  *   (tree_compress of the indexer streams).  idx_out [B, T, k] (optional)
  *   receives the selection, ascending and -1 padded (-1 where there is no node);

@@ -240,7 +240,8 @@ tree_compress_kernel(const __grid_constant__ TreeCompressParams p) {
     return;
   }
   // e4m3 codes with one fp32 scale per 128 channels, amax / 448 (1 for an
-  // all-zero block): the cache's rule, so that a committed key is the same
+  // all-zero block): the cache's rule (the pooled values are decode_compress's to
+  // some ulps, being summed in another order, and codes next to a border differ)
   // (nv is a multiple of 128 / VEC lanes, which divides a warp)
   constexpr int LB = 128 / VEC;
   if (tid < (nv + 31) / 32 * 32) {
