@@ -903,7 +903,10 @@ __global__ void __launch_bounds__(kTreeCombineThreads, 4) tree_combine_kernel(co
   // -1: no key, and no O)
   const float inv = z2 == INFINITY ? 0.f : 1.f / den;
   const auto weight = [&](int s, float m, float l) {
-    w_s[s][h] = l < 0.f ? -1.f : m == -INFINITY || z2 == INFINITY ? 0.f : l * exp2f(m - Ms) * inv;
+    // (formed whether or not there are keys: with l tested first, m was asked for a
+    // round trip later, 22.6 against 21.7 us for 3 nodes of 18 splits)
+    const float w = m == -INFINITY || z2 == INFINITY ? 0.f : l * exp2f(m - Ms) * inv;
+    w_s[s][h] = l < 0.f ? -1.f : w;
   };
   if (p.splits <= 16) {
 #pragma unroll
