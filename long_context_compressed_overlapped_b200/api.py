@@ -88,11 +88,11 @@ def indexer_topk(qI, w, kI, q_pos, m, k, *, kI_scale=None, idx=None, scores_out=
     Nk = kI.shape[1]
     if idx is None:
         idx = torch.empty(B, nq, k, dtype=torch.int32, device=qI.device)
-    w = _f32(w)
+    w, kI_scale = _f32(w), _f32(kI_scale)        # (locals: converted copies live until the launches)
     q_pos = q_pos.to(torch.int32).contiguous()
     args = N.IndexerArgs(q_dtype=_dt(qI), k_dtype=_dt(kI), B=B, nq=nq, HI=HI, dI=dI, N=Nk, m=m,
                          k=k, qI=_ptr(qI), w=_ptr(w), kI=_ptr(kI),
-                         kI_scale=_ptr(_f32(kI_scale)), q_pos=_ptr(q_pos), idx=_ptr(idx),
+                         kI_scale=_ptr(kI_scale), q_pos=_ptr(q_pos), idx=_ptr(idx),
                          scores_out=_ptr(scores_out), sel_scores=_ptr(sel_scores),
                          entry_base=int(entry_base))
     L = N.lib()
@@ -117,12 +117,13 @@ def compressed_attn_prefill(kind, q, kv_comp, kv_win, sinks, *, m, w, rope_dims,
     if out is None:
         out = torch.empty_like(q)
     kk = idx.shape[2] if idx is not None else 0
+    q_gain, kv_gain, sinks = _f32(q_gain), _f32(kv_gain), _f32(sinks)
     args = N.AttnArgs(kind=N.CSA if kind == "csa" else N.HCA, dtype=_dt(q), B=B, n=n, H=H, d=d,
                       N=Nc, m=m, k=kk, w=w, rope_dims=rope_dims, rope_base=rope_base, eps=eps,
                       scale=scale, q_norm=int(bool(q_norm)), kv_norm=int(bool(kv_norm)),
                       q=_ptr(q), kv_comp=_ptr(kv_comp) if Nc > 0 else None, kv_win=_ptr(kv_win),
-                      q_gain=_ptr(_f32(q_gain)), kv_gain=_ptr(_f32(kv_gain)),
-                      idx=_ptr(idx), sinks=_ptr(_f32(sinks)), out=_ptr(out))
+                      q_gain=_ptr(q_gain), kv_gain=_ptr(kv_gain),
+                      idx=_ptr(idx), sinks=_ptr(sinks), out=_ptr(out))
     L = N.lib()
     ws_bytes = L.csahca_prefill_workspace_size(C.byref(args))
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
