@@ -9,6 +9,7 @@ stream.  Every step of the path runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -42,6 +43,53 @@ def _f32(t):
     return None if t is None else t.contiguous().float()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _keep_for(stream, x):
+    """Tensors among x (nested): their memory stays theirs until the stream has read it."""
+    if isinstance(x, torch.Tensor):
+        if x.is_cuda:
+            x.record_stream(stream)
+    elif isinstance(x, (tuple, list, dict)):
+        for y in x.values() if isinstance(x, dict) else x:
+            _keep_for(stream, y)
+
+
+def _on(stream, dev, call, *args):
+    """call(*args) with the tensors' device current and the given stream (or
+    the device's current one) as the stream of its allocations and kernels.
+    On a stream that is not the current one the caller may drop the tensors
+    as soon as the call returns."""
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        _keep_for(stream, args)
+        with torch.cuda.stream(stream):
+            return call(*args)
+    if torch.cuda.current_device() == dev.index:
+        return call(*args)
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _streamed(call):
+    """A wrapper whose stream argument is handled by _on (the first tensor among
+    its arguments says which device): its workspace and converted copies belong
+    to the stream that reads them."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        dev = next((x.device for x in args if isinstance(x, torch.Tensor)), None)
+        if dev is None or dev.type != "cuda":
+            return call(*args, stream=stream, **kw)          # (refused there)
+        return _on(stream, dev, lambda a, k: call(*a, **k), args, kw)
+    return on
+
+
+@_streamed
 def _compress(kind, a, za, bias_a, m, *, b=None, zb=None, bias_b=None, gain=None,
               rms_norm=True, rope_dims=0, rope_base=10000.0, eps=1e-6, first_block=0,
               num_blocks=-1, out=None, stream=None):
@@ -74,6 +122,7 @@ def hca_compress(a, za, bias_a, m, **kw):
     return _compress("hca", a, za, bias_a, m, **kw)
 
 
+@_streamed
 def indexer_topk(qI, w, kI, q_pos, m, k, *, kI_scale=None, idx=None, scores_out=None,
                  sel_scores=None, entry_base=0, stream=None):
     """Lightning-indexer scores over the visible compressed keys and the
@@ -104,6 +153,7 @@ def indexer_topk(qI, w, kI, q_pos, m, k, *, kI_scale=None, idx=None, scores_out=
     return idx
 
 
+@_streamed
 def compressed_attn_prefill(kind, q, kv_comp, kv_win, sinks, *, m, w, rope_dims, idx=None,
                             q_gain=None, kv_gain=None, q_norm=True, kv_norm=True,
                             rope_base=10000.0, eps=1e-6, scale=0.0, out=None, stream=None):
@@ -173,6 +223,7 @@ def decode_args(kind, q, pos, kv_cache, win, sinks, *, m, rope_dims, k=0, qI=Non
     return args, out, keep
 
 
+@_streamed
 def compressed_attn_decode(kind, q, pos, kv_cache, win, sinks, *, m, rope_dims, k=0, qI=None,
                            wI=None, kI=None, kI_scale=None, idx_in=None, idx_out=None,
                            q_gain=None, q_norm=True, rope_base=10000.0, eps=1e-6, scale=0.0,
@@ -241,6 +292,7 @@ def decode_compress_args(kind, pos, streams, ring, kv_cache, *, m, bias_a, bias_
     return args, keep
 
 
+@_streamed
 def decode_compress(kind, pos, streams, ring, kv_cache, *, m, bias_a, stream=None, **kw):
     """One decode step of one layer's compressors: the new token's raw streams
     into the ring, its window row (if kv_raw and win are given) and, when the
@@ -256,6 +308,7 @@ def cp_partial_floats(H: int, d: int) -> int:
     return 2 * H + H * d
 
 
+@_streamed
 def cp_topk_merge(cand_idx, cand_scores, bases, rank, *, idx_global=None, idx_local=None, stream=None):
     """Stage 1 of context parallelism: the global top-k from every rank's
     candidates.  cand_idx / cand_scores [R, rows, k] (local rows and their
@@ -277,6 +330,7 @@ def cp_topk_merge(cand_idx, cand_scores, bases, rank, *, idx_global=None, idx_lo
     return idx_global, idx_local
 
 
+@_streamed
 def cp_attn_merge(partials, sinks, pos, *, H, d, rope_dims, dtype=torch.bfloat16, rope_base=10000.0,
                   out=None, stream=None):
     """Stage 2 of context parallelism: the layer output [rows, H, d] from the
@@ -291,39 +345,6 @@ def cp_attn_merge(partials, sinks, pos, *, H, d, rope_dims, dtype=torch.bfloat16
                          partials=_ptr(partials), sinks=_ptr(keep), pos=_ptr(pos), out=_ptr(out))
     N.check(N.lib().cp_attn_merge(C.byref(args), _stream(stream)), "cp_attn_merge")
     return out
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _keep_for(stream, x):
-    """Tensors among x (nested): their memory stays theirs until the stream has read it."""
-    if isinstance(x, torch.Tensor):
-        if x.is_cuda:
-            x.record_stream(stream)
-    elif isinstance(x, (tuple, list, dict)):
-        for y in x.values() if isinstance(x, dict) else x:
-            _keep_for(stream, y)
-
-
-def _on(stream, dev, call, *args):
-    """call(*args) with the tensors' device current and the given stream (or
-    the device's current one) as the stream of its allocations and kernels.
-    On a stream that is not the current one the caller may drop the tensors
-    as soon as the call returns."""
-    if dev.type != "cuda":
-        raise ValueError("tensors passed to the CUDA library must live on a CUDA device")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        _keep_for(stream, args)
-        with torch.cuda.stream(stream):
-            return call(*args)
-    if torch.cuda.current_device() == dev.index:
-        return call(*args)
-    with torch.cuda.device(dev):
-        return call(*args)
 
 
 def _arg(name, t, dev, shape, dtype, optional=False):
