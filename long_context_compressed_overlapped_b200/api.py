@@ -201,6 +201,7 @@ def decode_args(kind, q, pos, kv_cache, win, sinks, *, m, rope_dims, k=0, qI=Non
     keep.append(pos)
     if out is None and partial_out is None:
         out = torch.empty_like(q)
+    keep.append((q, kv_cache, win, qI, kI, idx_in, idx_out, out, partial_out))
     HI = dI = 0
     qI_dt = kI_dt = 0
     if qI is not None:
@@ -279,6 +280,7 @@ def decode_compress_args(kind, pos, streams, ring, kv_cache, *, m, bias_a, bias_
         dI = ia.shape[1]
         if kI is None or iring is None or ibias_a is None or ibias_b is None:
             raise ValueError("decode_compress: indexer streams need iring, ibias_a, ibias_b and kI")
+    keep.append((a, b, za, zb, kv_raw, ring, kv_cache, win, ia, ib, iza, izb, iring, kI, kI_scale))
     args = N.DecodeCompressArgs(
         kind=N.CSA if csa else N.HCA, dtype=_dt(a), B=B, d=d, m=m, N_cap=kv_cache.shape[1],
         w=win.shape[1] if win is not None else 0, rope_dims=rope_dims, rope_base=rope_base, eps=eps,
@@ -462,7 +464,7 @@ def tree_compress_args(kind, streams, ring, pos, parents, bias_a, m, *, bias_b=N
     if fresh:
         out = torch.empty(oshape, dtype=odt, device=dev)
     p = [_arg("streams", t, dev, shape, dt) for t in streams]
-    keep.append((streams, ring, pos, parents, bias_a, bias_b, gain, out, out_scale))
+    keep.append((*streams, ring, pos, parents, bias_a, bias_b, gain, out, out_scale))
     # (in the struct's order)
     a = N.TreeCompressArgs(
         N.CSA if csa else N.HCA, code, N.E4M3 if f8 else code, B, T, c, m, bool(rms_norm), rope_dims, rope_base, eps,

@@ -1,4 +1,4 @@
-"""The argument structs of the tree calls hold device pointers: the tensors that
+"""The argument structs of the decode and tree calls hold device pointers: the tensors that
 they point to stay alive with the list that comes with the struct, and a
 TreeStep's buffers are its own."""
 
@@ -42,6 +42,24 @@ def test_structs_keep_their_tensors():
     gc.collect()
     assert all(r() is not None for r in refs)
     del held
+
+
+def test_decode_structs_keep_their_tensors():
+    wl = synth.WORKLOADS["decode_1m"]
+    L = synth.decode_inputs(wl, DEV, ctx=1003, B=2, layers=("csa",))[0]
+    idx, out = torch.empty(2, wl.k, dtype=torch.int32, device=DEV), torch.empty_like(L["q"])
+    names = ("q", "pos", "kv", "win", "sinks", "qI", "w", "kI", "kI_scale", "q_gain")
+    refs = [weakref.ref(L[n]) for n in names] + [weakref.ref(idx), weakref.ref(out)]
+    held = api.decode_args("csa", L["q"], L["pos"], L["kv"], L["win"], L["sinks"], m=L["m"], rope_dims=wl.r, k=wl.k, qI=L["qI"], wI=L["w"],
+                           kI=L["kI"], kI_scale=L["kI_scale"], idx_out=idx, out=out, q_gain=L["q_gain"])
+    names = ("pos", "kv", "win", "ring", "iring", "ca", "cb", "cza", "czb", "ia", "ib", "iza", "izb", "kv_raw", "kI", "kI_scale",
+             "bias_a", "bias_b", "ibias_a", "ibias_b", "kv_gain")
+    refs += [weakref.ref(L[n]) for n in names]
+    comp = runtime.compress_args(wl, L)
+    del L, idx, out
+    gc.collect()
+    assert all(r() is not None for r in refs)
+    del held, comp
 
 
 def test_a_step_writes_its_own_buffers_only():
