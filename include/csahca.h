@@ -499,9 +499,9 @@ int cp_attn_merge(const csahca_cp_merge_args* args, void* stream);
  *   other).  HQ or HK = 0: that side is left out.
  *   The rows of a token with pos < 0 (padding) are left as they were, or written
  *   as zeros where zero_rest says so (bit 0: in q_out, bit 1: in k_out).
- * Constraints: B * n < 2^31, HQ + HK <= 65535; dtype F32 (d % 4 == 0, d <= 512) or BF16 (d % 8 == 0, d <=
- *   1024); rope_dims even, <= d and <= 512, (d - rope_dims) even.  No
- *   workspace. */
+ * Constraints: B * n < 2^31, HQ + HK <= 65535; dtype F32 (d % 4 == 0, d <=
+ *   512) or BF16 (d % 8 == 0, d <= 1024); rope_dims even, <= d and <= 512,
+ *   (d - rope_dims) even.  No workspace. */
 typedef struct {
   int32_t dtype;
   int32_t B, n, HQ, HK, d;

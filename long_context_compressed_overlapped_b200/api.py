@@ -82,7 +82,7 @@ def _streamed(call):
     to the stream that reads them."""
     @functools.wraps(call)
     def on(*args, stream=None, **kw):
-        dev = next((x.device for x in args if isinstance(x, torch.Tensor)), None)
+        dev = next((x.device for x in (*args, *kw.values()) if isinstance(x, torch.Tensor)), None)
         if dev is None or dev.type != "cuda":
             return call(*args, stream=stream, **kw)          # (refused there)
         return _on(stream, dev, lambda a, k: call(*a, **k), args, kw)

@@ -24,6 +24,8 @@ def cases():
     codes, scale = synth.quantize_e4m3_rows(normal(B, 3000, 128))
     yield "indexer_topk", lambda x, **kw: api.indexer_topk(x[0], x[1], x[2], x[3], m, 64, kI_scale=x[4], **kw), \
         [normal(B, 3, 64, 128), normal(B, 3, 64), codes, torch.full((B, 3), 12000, device=DEV), scale.double()]
+    yield "indexer_topk by name", lambda x, **kw: api.indexer_topk(qI=x[0], w=x[1], kI=x[2], q_pos=x[3], m=m, k=64, kI_scale=x[4], **kw), \
+        [normal(B, 3, 64, 128), normal(B, 3, 64), codes, torch.full((B, 3), 12000, device=DEV), scale.double()]
     yield "compressed_attn_prefill", lambda x, **kw: api.compressed_attn_prefill("hca", x[0], x[1], x[2], x[3], m=m, w=w, rope_dims=64,
                                                                                  q_gain=x[4], **kw), \
         [normal(1, n, 64, d), normal(1, n // m, d), normal(1, n, d), normal(64), normal(d)]
@@ -45,7 +47,7 @@ def cases():
         [normal(2, B, 2 * 4 + 4 * 64, dt=torch.float32).abs(), normal(4), pos]
 
 
-@pytest.mark.parametrize("name", ["csa_compress", "indexer_topk", "compressed_attn_prefill", "compressed_attn_decode", "decode_compress",
+@pytest.mark.parametrize("name", ["csa_compress", "indexer_topk", "indexer_topk by name", "compressed_attn_prefill", "compressed_attn_decode", "decode_compress",
                                   "cp_topk_merge", "cp_attn_merge"])
 def test_call_on_another_stream(name):
     call, args = next((c, a) for n, c, a in cases() if n == name)
